@@ -246,6 +246,152 @@ int fadkv_attend(const fadkv_dict *dict, int32_t layer, int32_t s, const int32_t
                  float scale, float *out, void *workspace, size_t workspace_bytes,
                  hipStream_t stream);
 
+/* ---- the dense cache beside the codes -----------------------------------------------------
+ * Tokens that are not coded (a prompt while it is prefilled, tokens waiting for the encoder)
+ * keep their keys and values in pages: blocks of page_size tokens, handed out to the rows
+ * (requests) of a batch as they grow.  Four calls work on them, in the order of a decode step:
+ * fadkv_pages_advance (lengths -> block table, slots, positions), fadkv_norm_rope (heads of a
+ * projection -> normed, rotated queries; keys and values into the pages and the encoder's rows),
+ * fadkv_attend_paged (one new token per row) or fadkv_attend_prompt (many).  They follow the
+ * conventions at the top of this file (streams, memory, errors); make the device that holds the
+ * buffers current before calling. */
+
+/* One layer's pages.  Token slot t = page * page_size + offset of KV head h is the d elements at
+ * k[page][h][offset] (and v). */
+typedef struct {
+  int32_t num_pages; /* num_pages * page_size < 2^31 */
+  int32_t page_size; /* 16, 32, 64, 128 or 256 tokens */
+  int32_t kv_heads;  /* 1 .. 256 */
+  int32_t d;         /* 64 or 128 */
+  int32_t dtype;     /* fadkv_dtype of keys, values and queries */
+  void *k;           /* device [num_pages][kv_heads][page_size][d], 16-byte aligned */
+  void *v;           /* as k */
+} fadkv_pages;
+
+/* row status of fadkv_pages_advance */
+#define FADKV_ROW_OK 0
+#define FADKV_ROW_REFUSED 1  /* its new tokens did not fit: nothing of the row changed */
+#define FADKV_ROW_RELEASED 2 /* ended: its pages are free from the next call on */
+
+/* One step of a paged cache's bookkeeping, on the GPU, from the number of tokens each row adds.
+ * Row r held lens[r] tokens in the pages table[r][0 .. ceil(lens[r] / page_size)).
+ *   new_lens[r] > 0: its new tokens go behind them, on pages taken from the free ring in row order;
+ *   new_lens[r] = 0: nothing changes;
+ *   new_lens[r] < 0: the row has ended: its pages go to the ring's tail in row and page order,
+ *     to be taken from the next call on, and its length becomes 0.
+ * A row is refused (its length and pages stay as they were) if the pages that it and the rows
+ * before it need are more than are free, if it would outgrow max_pages, or if its tokens end
+ * past max_tokens.  The pages that refused rows need count for the rows behind them too, except
+ * those of rows that outgrow max_pages.
+ *   new_lens, lens  device int32 [R]; lens is taken as clamped to [0, max_pages * page_size]
+ *   table           device int32 [R][max_pages]: entries of new pages are written, no others
+ *   ring            device int32 [num_pages]: free page ids in entries ring_state[0],
+ *                   ring_state[0] + 1, ... (mod num_pages), ring_state[1] of them
+ *   lens_out [R], ring_state_out [2]  the new lengths and state (may be lens and ring_state)
+ *   cu              device int32 [R+1]: row r's new tokens are tokens cu[r] .. cu[r+1] - 1 of the
+ *                   packed batch (prefix sums of max(new_lens, 0), refused rows included, at
+ *                   most max_tokens)
+ *   status          device int32 [R]: FADKV_ROW_*
+ *   slots, positions  device int32 [max_tokens]: every new token's slot (-1 in a refused row) and
+ *                   its position in the row; both -1 behind the last new token (a padded batch)
+ * The arrays are distinct except as said.  0 <= R <= 8192, num_pages * page_size < 2^31, 1 <=
+ * max_pages, max_pages * page_size + max_tokens < 2^31, R * max_pages < 2^31.
+ * workspace: fadkv_pages_workspace_bytes(R), 4-byte aligned. */
+int fadkv_pages_workspace_bytes(int64_t R, size_t *bytes);
+int fadkv_pages_advance(int32_t num_pages, int32_t page_size, int64_t R, int32_t max_pages,
+                        const int32_t *new_lens, const int32_t *lens, int32_t *table,
+                        int32_t *ring, const int32_t *ring_state, int64_t max_tokens,
+                        int32_t *lens_out, int32_t *ring_state_out, int32_t *cu, int32_t *status,
+                        int32_t *slots, int32_t *positions, void *workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/* Frequencies of rotary positions, angle = position * freqs[i] for pair i, written to HOST
+ * memory (rot_dim / 2 doubles; copy them to the device for fadkv_norm_rope).  base^(-2i/rot_dim),
+ * then for long contexts
+ *   FADKV_ROPE_LINEAR: divided by factor (position interpolation);
+ *   FADKV_ROPE_BANDS:  by wavelength w = 2 pi / f against the original context length L: kept for
+ *     w < L / high, divided by factor for w > L / low, between them a mix of both, linear in
+ *     L / w (the scaling of the Llama-3.1 and 3.2 models: low 1, high 4, L 8192);
+ *   FADKV_ROPE_YARN:   YaRN (arXiv 2309.00071, section 3.2): kept for pairs that turn more than
+ *     high times within L, divided by factor below low turns, between them a mix of both, linear
+ *     in the pair index between the two rounded outwards (low 1, high 32).
+ * *mscale: what queries and keys are multiplied by: 0.1 ln(factor) + 1 for YARN with factor > 1,
+ * else 1.  base > 1, factor >= 1, 0 < low < high, original_len >= 1 (the last three for the two
+ * kinds that use them). */
+typedef enum {
+  FADKV_ROPE_PLAIN = 0,
+  FADKV_ROPE_LINEAR = 1,
+  FADKV_ROPE_BANDS = 2,
+  FADKV_ROPE_YARN = 3
+} fadkv_rope_kind;
+int fadkv_rope_freqs(int32_t rot_dim, double base, int32_t kind, double factor, double low,
+                     double high, double original_len, double *freqs, double *mscale);
+
+/* The heads of n tokens, as a projection leaves them. */
+typedef struct {
+  int64_t n;              /* tokens, padding included, 0 .. 2^24 */
+  int32_t heads;          /* query heads, 1 .. 16384 */
+  int32_t kv_heads;       /* key and value heads, 1 .. 256 */
+  int32_t d;              /* 64 or 128 */
+  int32_t dtype;          /* fadkv_dtype */
+  const void *q;          /* device [n][heads][d], tokens q_stride elements apart */
+  const void *k, *v;      /* device [n][kv_heads][d], tokens k_stride, v_stride apart */
+  int64_t q_stride, k_stride, v_stride; /* >= heads * d (kv_heads * d), 16-byte multiples */
+  const int32_t *positions; /* device [n]; negative: a padding token, of which nothing is written */
+  const void *q_weight, *k_weight; /* device [d] in dtype, or null: no norm */
+  float eps;              /* >= 0 */
+  const double *freqs;    /* device [rot_dim / 2], radians a position; null if rot_dim is 0 */
+  int32_t rot_dim;        /* the first rot_dim elements are rotated: a multiple of 16, 0 .. d */
+  int32_t interleaved;    /* pairs (2i, 2i+1) if 1, (i, i + rot_dim/2) if 0 */
+  float mscale;           /* factor on the rotated part, finite */
+} fadkv_qkv;
+
+/* Norm and rotation of every query and key head, and the cache write, in one pass:
+ *   y = w * x / sqrt(mean(x^2) + eps) (where a weight is given), then pair (a, b) becomes
+ *   mscale * (a cos - b sin, b cos + a sin) with angle = position * freqs[i].
+ *   q_out   device [n][heads][d] (may be q where q_stride = heads * d)
+ *   pages, slots  null, or: token i's keys and values go to slot slots[i] (device int32 [n]; a
+ *           slot outside [0, num_pages * page_size) is not written; no slot twice)
+ *   k_rows, v_rows  null, or device [kv_heads][n][d]: rows in (head, token) order, the encoder's
+ *           X of the layer's key and value dictionary
+ * All 16-byte aligned.  The outputs must not overlap the inputs (but q_out, as said) or each
+ * other.  fp32 throughout (angles are reduced in fp64, for far positions), rounded once. */
+int fadkv_norm_rope(const fadkv_qkv *in, void *q_out, const fadkv_pages *pages,
+                    const int32_t *slots, void *k_rows, void *v_rows, hipStream_t stream);
+
+/* Attention of one new token per row over the pages:
+ *   out[r][h] = sum_t p_t v_t, p = softmax_t(scale * <q[r][h], k_t>) over the visible tokens,
+ * k_t and v_t those of KV head h / (heads / kv_heads).  Visible to a query at position i: tokens
+ * t <= i with t > i - window or t < sinks (window 0: all t <= i).  The query is the row's last
+ * token, i = lens[r] - 1, whose key and value are in the pages already.  A row without tokens
+ * gives 0; tokens of a page id outside [0, num_pages) count as not visible.  What lies in pages
+ * behind a row's length is never used, whatever it holds.
+ *   table device int32 [R][max_pages]; lens device int32 [R], clamped to [0, max_pages * page_size]
+ *   q, out  device [R][heads][d] in pages->dtype, 16-byte aligned, distinct
+ *   max_len an upper bound of lens that sizes the split over the length (any larger length is
+ *           still right, only slower); 1 .. max_pages * page_size
+ * heads a multiple of kv_heads, heads / kv_heads <= 64, R * heads <= 2^22, window >= 0,
+ * sinks >= 0, scale finite.  Scores and sums are fp32; the weights p are rounded to dtype for the
+ * product with v.  Results do not depend on the run (no atomics).  workspace:
+ * fadkv_attend_paged_workspace_bytes() bytes (0 where no split is needed), 256-byte aligned. */
+int fadkv_attend_paged_workspace_bytes(const fadkv_pages *pages, int64_t R, int32_t heads,
+                                       int32_t max_len, size_t *bytes);
+int fadkv_attend_paged(const fadkv_pages *pages, const int32_t *table, int32_t max_pages,
+                       const int32_t *lens, int64_t R, const void *q, int32_t heads, float scale,
+                       int32_t window, int32_t sinks, int32_t max_len, void *out,
+                       void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The same for many new tokens per row, packed: tokens cu[r] .. cu[r+1] - 1 of q are the last
+ * ones of row r's lens[r] tokens, each attends causally (its visible tokens as above, by its own
+ * position); a query whose position would be negative gives 0.
+ *   cu device int32 [R+1], non-decreasing, cu[0] >= 0, taken as clamped to [0, n]
+ *   q, out device [n][heads][d]; rows of out that belong to no token of a row stay as they were
+ * n * heads <= 2^28; the other limits as above.  Needs no workspace. */
+int fadkv_attend_prompt(const fadkv_pages *pages, const int32_t *table, int32_t max_pages,
+                        const int32_t *lens, const int32_t *cu, int64_t R, const void *q,
+                        int64_t n, int32_t heads, float scale, int32_t window, int32_t sinks,
+                        void *out, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *fadkv_status_string(int status);
 

@@ -1,0 +1,213 @@
+// Attention of one new token per row over paged keys and values.
+//
+// out = sum_t p_t v_t, p = softmax_t(scale <q, k_t>), in one pass over the visible tokens with a
+// running maximum and sum.  What bounds it: HBM.  Every visible key and value is read once, by
+// one wave, for all query heads of its kv head (up to 16 columns of the matrix instruction), at
+// 4 d heads / (4 d kv_heads) = one to a few flops a byte.
+//
+// A row's 32-token tiles are split over `splits` workgroups (as many as fill the chip, counted
+// from the longest length; each takes an equal share of the row's own length) and dealt to a
+// workgroup's four waves in turn.  The waves' (maximum, sum, output) are joined in LDS, the
+// workgroups' through the workspace by a second kernel.
+#include "attend_tile.h"
+
+namespace fadkv {
+
+namespace {
+
+constexpr int AP_WAVES = 4;
+constexpr int AP_TARGET = 1024;   // workgroups to aim for: four on each of the 256 CUs
+constexpr int AP_LEAST = 256;     // tokens below which a workgroup's share is not cut further
+
+}  // namespace
+
+int attend_paged_splits(int64_t R, int32_t kv_heads, int32_t group, int64_t visible) {
+  const int64_t wgs = R * kv_heads * ((group + 15) / 16);
+  int64_t s = wgs > 0 ? (AP_TARGET + wgs - 1) / wgs : 1;
+  const int64_t most = (visible + AP_LEAST - 1) / AP_LEAST;
+  s = s < most ? s : most;
+  return (int)(s < 1 ? 1 : s);
+}
+
+// the visible tiles of a row: those of the first tokens, then those of the window
+struct TileList {
+  int first, from, count;   // tiles [0, first), then [from, from + count - first)
+};
+
+__device__ __forceinline__ TileList tiles_of(int len, int window, int sinks) {
+  TileList tl;
+  const int last = (len + 31) >> 5;
+  const int lo = window < len ? (len - window) >> 5 : 0;
+  const int sk = sinks < len ? sinks : len;
+  tl.first = (sk + 31) >> 5;
+  if (tl.first >= lo) {   // they meet: one stretch
+    tl.first = 0;
+    tl.from = sk > 0 ? 0 : lo;
+  } else {
+    tl.from = lo;
+  }
+  tl.count = tl.first + last - tl.from;
+  return tl;
+}
+
+template <int DT, int D, bool SPLIT>
+__global__ __launch_bounds__(64 * AP_WAVES) void attend_paged_kernel(AttendArgs a) {
+  using T = AttTile<DT, D>;
+  __shared__ __attribute__((aligned(16))) float s_o[AP_WAVES][16][D + 4];
+  __shared__ float s_m[AP_WAVES][16], s_l[AP_WAVES][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // kv head fastest: workgroups of one kv head land on one chiplet (8 heads, 8 chiplets)
+  const int blocks = (a.group + 15) >> 4;
+  unsigned b = blockIdx.x;
+  const int head = (int)(b % a.kv_heads);
+  b /= a.kv_heads;
+  const int cb = (int)(b % blocks);
+  b /= blocks;
+  const int split = SPLIT ? (int)(b % a.splits) : 0;
+  const int r = (int)(SPLIT ? b / a.splits : b);
+  const int heads = a.kv_heads * a.group;
+
+  const int64_t room = (int64_t)a.max_pages << a.page_shift;
+  int len = a.lens[r];
+  len = len < 0 ? 0 : ((int64_t)len > room ? (int)room : len);
+  const TileList tl = tiles_of(len, a.window, a.sinks);
+  const int share = SPLIT ? (tl.count + a.splits - 1) / a.splits : tl.count;
+  const int i0 = SPLIT ? split * share : 0;
+  const int i1 = i0 + share < tl.count ? i0 + share : tl.count;
+
+  const int col = lane & 15;
+  const int gq = cb * 16 + col;
+  const bool there = gq < a.group;
+  const uint8_t *qrow = static_cast<const uint8_t *>(a.q) +
+                        ((size_t)r * heads + (size_t)head * a.group + (there ? gq : 0)) * T::ROWB;
+  uint4 q[T::CH];
+  load_queries<DT, D>(qrow, there, lane, q);
+  PageView pv = {static_cast<const uint8_t *>(a.k), static_cast<const uint8_t *>(a.v),
+                 a.table + (size_t)r * a.max_pages, a.num_pages, a.page_shift, a.kv_heads, head,
+                 a.max_pages};
+  const Visible see = {a.window < len ? len - a.window : 0, len};
+  const float scale2 = a.scale * kLog2e;
+
+  AttState<DT, D> st;
+  st.clear();
+  for (int i = i0 + wave; i < i1; i += AP_WAVES) {
+    const int t0 = (i < tl.first ? i : tl.from + i - tl.first) << 5;
+    KvTile<DT, D> kv;
+    kv.load(pv, t0, lane);
+    const bool whole = kv.there[0] && kv.there[1] && t0 + 32 <= see.hi &&
+                       (t0 >= see.lo || t0 + 32 <= a.sinks);
+    attend_tile<DT, D>(kv, q, t0, whole, see, see, a.sinks, scale2, lane, st);
+  }
+
+  // join the waves
+  const float l = column_sum(st.l);
+  const int g = lane >> 4;
+#pragma unroll
+  for (int e = 0; e < T::EP; ++e)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_o[wave][col][T::EP * (4 * g + i) + e] = st.o[e][i];
+  if (g == 0) {
+    s_m[wave][col] = st.m;
+    s_l[wave][col] = l;
+  }
+  __syncthreads();
+  const int here = a.group - cb * 16 < 16 ? a.group - cb * 16 : 16;
+  for (int i = tid; i < here * (D / 4); i += 64 * AP_WAVES) {
+    const int c = i / (D / 4), d4 = i % (D / 4);
+    float m = s_m[0][c];
+#pragma unroll
+    for (int w = 1; w < AP_WAVES; ++w) m = fmaxf(m, s_m[w][c]);
+    const float base = m == -__builtin_inff() ? 0.f : m;
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < AP_WAVES; ++w) {
+      const float f = __builtin_amdgcn_exp2f(s_m[w][c] - base);
+      const float4 x = *reinterpret_cast<const float4 *>(&s_o[w][c][4 * d4]);
+      sum = fmaf(s_l[w][c], f, sum);
+      o.x = fmaf(x.x, f, o.x);
+      o.y = fmaf(x.y, f, o.y);
+      o.z = fmaf(x.z, f, o.z);
+      o.w = fmaf(x.w, f, o.w);
+    }
+    const size_t qi = (size_t)r * heads + (size_t)head * a.group + cb * 16 + c;
+    if constexpr (SPLIT) {
+      const size_t at = qi * a.splits + split;
+      reinterpret_cast<float4 *>(a.part_o + at * D)[d4] = o;
+      if (d4 == 0) a.part_ml[at] = make_float2(m, sum);
+    } else {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;   // no visible token: 0
+      if constexpr (DT == DT_F32) {
+        reinterpret_cast<float4 *>(a.out)[qi * (D / 4) + d4] =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      } else {
+        reinterpret_cast<uint2 *>(a.out)[qi * (D / 4) + d4] =
+            make_uint2(round2<DT>(o.x * inv, o.y * inv), round2<DT>(o.z * inv, o.w * inv));
+      }
+    }
+  }
+}
+
+// out[query] = the splits' outputs, each scaled from its own maximum to the common one, over the
+// sum; one wave per query, the splits in order
+template <int DT, int D>
+__global__ __launch_bounds__(64) void attend_join_kernel(AttendArgs a) {
+  const size_t qi = blockIdx.x;
+  const int lane = threadIdx.x;
+  const float2 *ml = a.part_ml + qi * a.splits;
+  float m = -__builtin_inff();
+  for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, ml[s].x);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  const float base = m == -__builtin_inff() ? 0.f : m;
+  constexpr int E = D / 64;
+  float acc[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const float *po = a.part_o + qi * a.splits * D + lane * E;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 x = ml[s];
+    const float f = __builtin_amdgcn_exp2f(x.x - base);
+    sum = fmaf(x.y, f, sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(po[(size_t)s * D + e], f, acc[e]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const size_t at = qi * D + lane * E + e;
+    const float y = acc[e] * inv;
+    if constexpr (DT == DT_F32) static_cast<float *>(a.out)[at] = y;
+    else static_cast<uint16_t *>(a.out)[at] = (uint16_t)round2<DT>(y, 0.f);
+  }
+}
+
+template <int DT, int D> static void attend_paged_run(const AttendArgs &a, hipStream_t stream) {
+  const unsigned wgs = (unsigned)((size_t)a.R * a.kv_heads * ((a.group + 15) / 16));
+  if (a.splits > 1) {
+    hipLaunchKernelGGL((attend_paged_kernel<DT, D, true>), dim3(wgs * a.splits),
+                       dim3(64 * AP_WAVES), 0, stream, a);
+    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3((unsigned)(a.R * a.kv_heads * a.group)),
+                       dim3(64), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((attend_paged_kernel<DT, D, false>), dim3(wgs), dim3(64 * AP_WAVES), 0,
+                       stream, a);
+  }
+}
+
+hipError_t launch_attend_paged(int dtype, int d, const AttendArgs &a, hipStream_t stream) {
+  if (dtype == DT_F32) {
+    if (d == 64) attend_paged_run<DT_F32, 64>(a, stream);
+    else attend_paged_run<DT_F32, 128>(a, stream);
+  } else if (dtype == DT_F16) {
+    if (d == 64) attend_paged_run<DT_F16, 64>(a, stream);
+    else attend_paged_run<DT_F16, 128>(a, stream);
+  } else {
+    if (d == 64) attend_paged_run<DT_BF16, 64>(a, stream);
+    else attend_paged_run<DT_BF16, 128>(a, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace fadkv

@@ -1,0 +1,258 @@
+// One wave's work on 32 cached tokens for 16 query columns (gfx950, wave64): the part that the
+// paged attention kernels share.
+//
+// Scores come transposed, S^T = K Q^T: the A operand's rows are 16 keys and the B operand's columns
+// the 16 queries, so after the product lane l holds, for query l % 16, the scores of keys
+// 4 (l / 16) + e.  The sum over keys in O^T = V^T P^T may run in any order, so the four values a
+// lane holds of each of two 16-key groups are its eight entries of the second product's B
+// operand as they stand: p never moves between lanes.  A column's maximum needs two exchanges
+// (lanes l, l ^ 16, l ^ 32), its sum none until the end, and rescaling O is per lane.
+//
+// The A operand of the second product wants, per lane, eight keys of one element d.  A lane reads
+// d / 16 neighbouring elements (16 bytes at d = 128 in 16 bits) of each of its eight keys, which is
+// a coalesced read of whole rows, and transposes them in registers: operand e takes element e of
+// the eight.  Output row r of product e is then element (d / 16) r + e, so the lane ends up with
+// d / 4 neighbouring elements of its query's output.  No LDS, no barrier in the loop.
+#pragma once
+
+#include "common.h"
+#include "dense.h"
+
+namespace fadkv {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+template <int DT, int D> struct AttTile {
+  static constexpr int ES = Elem<DT>::bytes;
+  static constexpr int ROWB = D * ES;
+  static constexpr int CH = ROWB / 64;    // 16-byte chunks of a q or k row per lane
+  static constexpr int EP = D / 16;       // neighbouring elements of a v row per lane
+  static constexpr int VW = EP * ES / 4;  // their 32-bit words
+};
+
+// pages of one kv head: byte offsets of 16-token groups
+struct PageView {
+  const uint8_t *k, *v;
+  const int32_t *table;   // of the row
+  int num_pages, page_shift, kv_heads, head, max_pages;
+};
+
+// byte offset of the 16 tokens from t0 (a multiple of 16; the same for all lanes), or -1 where no
+// valid page holds them
+template <int ROWB> __device__ __forceinline__ int64_t group_at(const PageView &pv, int t0) {
+  const int pg = t0 >> pv.page_shift;
+  if (t0 < 0 || pg >= pv.max_pages) return -1;
+  const int id = __builtin_amdgcn_readfirstlane(pv.table[pg]);
+  if (id < 0 || id >= pv.num_pages) return -1;
+  const int off = t0 & ((1 << pv.page_shift) - 1);
+  return (int64_t)(((((size_t)id * pv.kv_heads + pv.head) << pv.page_shift) + off) * ROWB);
+}
+
+template <int DT>
+__device__ __forceinline__ void mfma16(const uint4 &a, const uint4 &b, f32x4_t &c) {
+  if constexpr (DT == DT_F16) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a),
+                                               __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  } else if constexpr (DT == DT_BF16) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  } else {
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+  }
+}
+
+// two floats to one word of 16-bit values, round to nearest even
+template <int DT> __device__ __forceinline__ uint32_t round2(float a, float b) {
+  if constexpr (DT == DT_F16) {
+    half2_t h;
+    h[0] = (_Float16)a;
+    h[1] = (_Float16)b;
+    return __builtin_bit_cast(uint32_t, h);
+  } else {
+    bf16x2_t h;
+    h[0] = (__bf16)a;
+    h[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, h);
+  }
+}
+
+// what a column sees: tokens [lo, hi) and [0, min(sinks, hi))
+struct Visible {
+  int lo, hi;
+};
+
+__device__ __forceinline__ bool sees(const Visible &s, int sinks, int t) {
+  return t < s.hi && (t >= s.lo || t < sinks);
+}
+
+template <int DT, int D> struct AttState {
+  f32x4_t o[AttTile<DT, D>::EP];
+  float m, l;   // running maximum (of scores times scale log2 e) and this lane's share of the sum
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int e = 0; e < AttTile<DT, D>::EP; ++e) o[e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    m = -__builtin_inff();
+    l = 0.f;
+  }
+};
+
+// keys and values of 32 tokens in registers
+template <int DT, int D> struct KvTile {
+  uint4 k[2][AttTile<DT, D>::CH];
+  uint32_t v[8][AttTile<DT, D>::VW];
+  bool there[2];
+
+  // Groups without a valid page read as zeros and are masked by the caller
+  __device__ __forceinline__ void load(const PageView &pv, int t0, int lane) {
+    using T = AttTile<DT, D>;
+    const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      const int64_t at = group_at<T::ROWB>(pv, t0 + 16 * a);
+      there[a] = at >= 0;
+      if (there[a]) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(pv.k + at + (size_t)r * T::ROWB);
+#pragma unroll
+        for (int i = 0; i < T::CH; ++i) k[a][i] = src[4 * i + g];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t *row =
+              reinterpret_cast<const uint32_t *>(pv.v + at + (size_t)(4 * g + e) * T::ROWB) + r * T::VW;
+          uint32_t *dst = v[4 * a + e];
+          if constexpr (T::VW == 2) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(row);
+            dst[0] = w.x; dst[1] = w.y;
+          } else {
+#pragma unroll
+            for (int c = 0; c < T::VW / 4; ++c) {
+              const uint4 w = reinterpret_cast<const uint4 *>(row)[c];
+              dst[4 * c] = w.x; dst[4 * c + 1] = w.y; dst[4 * c + 2] = w.z; dst[4 * c + 3] = w.w;
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < T::CH; ++i) k[a][i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < T::VW; ++c) v[4 * a + e][c] = 0;
+      }
+    }
+  }
+};
+
+// One tile against the wave's 16 columns.  `whole`: every column sees all 32 tokens (uniform).
+// Tokens that no column sees are zeroed in v: p = 0 does not undo an infinity or NaN there.
+template <int DT, int D>
+__device__ __forceinline__ void attend_tile(KvTile<DT, D> &kv, const uint4 (&q)[AttTile<DT, D>::CH],
+                                            int t0, bool whole, const Visible &col,
+                                            const Visible &any, int sinks, float scale2, int lane,
+                                            AttState<DT, D> &st) {
+  using T = AttTile<DT, D>;
+  const int g = lane >> 4;
+  f32x4_t s[2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    s[a] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < T::CH; ++i) mfma16<DT>(kv.k[a][i], q[i], s[a]);
+  }
+  float z[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) z[j] = s[j >> 2][j & 3] * scale2;
+  if (!whole) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
+      if (!kv.there[j >> 2] || !sees(col, sinks, t)) z[j] = -__builtin_inff();
+      if (!sees(any, sinks, t)) {
+#pragma unroll
+        for (int c = 0; c < T::VW; ++c) kv.v[j][c] = 0;
+      }
+    }
+  }
+  float top = z[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) top = fmaxf(top, z[j]);
+  top = fmaxf(top, __shfl_xor(top, 16, 64));
+  top = fmaxf(top, __shfl_xor(top, 32, 64));
+  const float m = fmaxf(st.m, top);
+  const float base = m == -__builtin_inff() ? 0.f : m;   // nothing visible yet: all weights are 0
+  const float keep = __builtin_amdgcn_exp2f(st.m - base);
+  st.m = m;
+  float p[8], sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    p[j] = __builtin_amdgcn_exp2f(z[j] - base);
+    sum += p[j];
+  }
+  st.l = fmaf(st.l, keep, sum);
+#pragma unroll
+  for (int e = 0; e < T::EP; ++e)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st.o[e][i] *= keep;
+  if constexpr (DT == DT_F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < T::EP; ++e)
+        st.o[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kv.v[j][e]), p[j], st.o[e], 0, 0, 0);
+  } else {
+    const uint4 pb = make_uint4(round2<DT>(p[0], p[1]), round2<DT>(p[2], p[3]),
+                                round2<DT>(p[4], p[5]), round2<DT>(p[6], p[7]));
+#pragma unroll
+    for (int e = 0; e < T::EP; ++e) {
+      // bytes 1:0 (e even) or 3:2 (e odd) of two keys' words
+      constexpr uint32_t kLo = 0x05040100u, kHi = 0x07060302u;
+      const uint32_t sel = (e & 1) ? kHi : kLo;
+      const uint4 va = make_uint4(__builtin_amdgcn_perm(kv.v[1][e / 2], kv.v[0][e / 2], sel),
+                                  __builtin_amdgcn_perm(kv.v[3][e / 2], kv.v[2][e / 2], sel),
+                                  __builtin_amdgcn_perm(kv.v[5][e / 2], kv.v[4][e / 2], sel),
+                                  __builtin_amdgcn_perm(kv.v[7][e / 2], kv.v[6][e / 2], sel));
+      mfma16<DT>(va, pb, st.o[e]);
+    }
+  }
+}
+
+// the 16 queries' B operand; lanes of an absent column hold zeros
+template <int DT, int D>
+__device__ __forceinline__ void load_queries(const uint8_t *row, bool there, int lane,
+                                             uint4 (&q)[AttTile<DT, D>::CH]) {
+  const uint4 *src = reinterpret_cast<const uint4 *>(row);
+#pragma unroll
+  for (int i = 0; i < AttTile<DT, D>::CH; ++i)
+    q[i] = there ? src[4 * i + (lane >> 4)] : make_uint4(0, 0, 0, 0);
+}
+
+// a column's sum over its four lanes
+__device__ __forceinline__ float column_sum(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// element i of a lane's D / 4 output elements: product i % EP, row entry i / EP
+template <int DT, int D>
+__device__ __forceinline__ void store_output(uint8_t *row, int lane, const float (&x)[D / 4]) {
+  if constexpr (DT == DT_F32) {
+    float4 *dst = reinterpret_cast<float4 *>(row) + (lane >> 4) * (D / 16);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+      dst[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+  } else {
+    uint4 *dst = reinterpret_cast<uint4 *>(row) + (lane >> 4) * (D / 32);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      dst[c] = make_uint4(round2<DT>(x[8 * c], x[8 * c + 1]), round2<DT>(x[8 * c + 2], x[8 * c + 3]),
+                          round2<DT>(x[8 * c + 4], x[8 * c + 5]),
+                          round2<DT>(x[8 * c + 6], x[8 * c + 7]));
+  }
+}
+
+}  // namespace fadkv

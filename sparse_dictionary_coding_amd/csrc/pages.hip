@@ -1,0 +1,226 @@
+// Paged-cache bookkeeping: request lengths -> block table, slots, positions.
+//
+// With P tokens a page, row r needs ceil((len + new) / P) - ceil(len / P) new pages; where they sit
+// in the free ring, where the row's tokens sit in the packed batch and where released pages go
+// are three prefix sums over the rows.  Released pages are appended behind the free ones, so the
+// entries that are read (the ring's head) and written (behind its tail) never meet and the rows
+// can be filled in any order.
+//
+// What bounds it: latency.  A step moves a few KB, so the time is the launches and the chain
+// length -> sums -> ring entry -> table and slot.  Small batches run as ONE workgroup that keeps
+// the sums and row records in LDS and fills everything itself; larger ones scan with one
+// workgroup and fill with many (tokens by a binary search of their row in an LDS copy of cu,
+// pages with one wave per row).
+#include "common.h"
+#include "dense.h"
+
+namespace fadkv {
+
+namespace {
+
+constexpr int SCAN_THREADS = 1024;
+constexpr int FILL_THREADS = 256;
+constexpr int FILL_TOKENS = 4 * FILL_THREADS;   // tokens per fill workgroup
+constexpr int MAX_ROWS = 8192;                  // rows of one call: their cu fits LDS (32 KB)
+constexpr int ONE_ROWS = SCAN_THREADS;          // one-workgroup form: a row per thread,
+constexpr int ONE_TOKENS = 4 * SCAN_THREADS;    // and a few tokens per thread
+
+struct Sums {
+  long long add, need, back;
+};
+
+__device__ __forceinline__ long long shfl_up_ll(long long v, int o) { return __shfl_up(v, o, 64); }
+
+// inclusive sums over the workgroup's threads of three values, carried in `carry`
+__device__ __forceinline__ Sums block_scan(Sums v, Sums &carry, Sums *s_wave) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const Sums u = {shfl_up_ll(v.add, o), shfl_up_ll(v.need, o), shfl_up_ll(v.back, o)};
+    if (lane >= o) {
+      v.add += u.add;
+      v.need += u.need;
+      v.back += u.back;
+    }
+  }
+  if (lane == 63) s_wave[wave] = v;
+  __syncthreads();
+  Sums before = carry, total = carry;
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
+    const Sums u = s_wave[w];
+    if (w < wave) {
+      before.add += u.add;
+      before.need += u.need;
+      before.back += u.back;
+    }
+    total.add += u.add;
+    total.need += u.need;
+    total.back += u.back;
+  }
+  __syncthreads();
+  carry = total;
+  return {v.add + before.add, v.need + before.need, v.back + before.back};
+}
+
+__device__ __forceinline__ int wrapped(int at, int num) { return at >= num ? at - num : at; }
+
+// slot and position of packed token j, which is in row r (cu[r] <= j < cu[r+1]) or in none
+__device__ __forceinline__ void fill_token(const PagesArgs &a, int j, int r, bool in, int begin,
+                                           const PageRow &row) {
+  int slot = -1, pos = -1;
+  if (in) {
+    pos = row.old + (j - begin);
+    if (row.ok) {
+      const int P = 1 << a.page_shift;
+      const int held = (int)(((int64_t)row.old + P - 1) >> a.page_shift);
+      const int pg = pos >> a.page_shift;
+      const int id = pg < held ? a.table[(size_t)r * a.max_pages + pg]
+                               : a.ring[wrapped(row.first + (pg - held), a.num_pages)];
+      if (id >= 0 && id < a.num_pages) slot = (id << a.page_shift) + (pos & (P - 1));
+    }
+  }
+  a.slots[j] = slot;
+  a.positions[j] = pos;
+}
+
+// the row's new pages into its table, or its released ones into the ring (one wave)
+__device__ __forceinline__ void fill_pages(const PagesArgs &a, int r, const PageRow &row, int lane) {
+  int32_t *tab = a.table + (size_t)r * a.max_pages;
+  if (row.pages > 0) {
+    const int held = (int)(((int64_t)row.old + (1 << a.page_shift) - 1) >> a.page_shift);
+    for (int i = lane; i < row.pages; i += 64)
+      tab[held + i] = a.ring[wrapped(row.first + i, a.num_pages)];
+  } else {
+    for (int i = lane; i < -1 - row.pages; i += 64)
+      a.ring[wrapped(row.first + i, a.num_pages)] = tab[i];
+  }
+}
+
+// rows [0, R) of cu that end at or before j: the row of token j
+__device__ __forceinline__ int row_of(const int *cu, int R, int j) {
+  int lo = 0, hi = R;   // smallest r with cu[r + 1] > j
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid + 1] <= j) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace
+
+template <bool ONE>
+__global__ __launch_bounds__(SCAN_THREADS) void pages_scan_kernel(PagesArgs a) {
+  __shared__ Sums s_wave[SCAN_THREADS / 64];
+  __shared__ int s_taken;
+  __shared__ int s_cu[ONE ? ONE_ROWS + 1 : 1];
+  __shared__ PageRow s_row[ONE ? ONE_ROWS : 1];
+  const int tid = threadIdx.x;
+  const int P = 1 << a.page_shift;
+  const long long room = (long long)a.max_pages << a.page_shift;
+  int head = a.ring_state[0], count = a.ring_state[1];
+  head = head < 0 || head >= a.num_pages ? 0 : head;
+  count = count < 0 ? 0 : (count > a.num_pages ? a.num_pages : count);
+  if (tid == 0) {
+    s_taken = 0;
+    a.cu[0] = 0;
+    if constexpr (ONE) s_cu[0] = 0;
+  }
+  Sums carry = {0, 0, 0};
+  __syncthreads();   // every thread has read ring_state, which ring_state_out may be
+  for (int r0 = 0; r0 < a.R; r0 += (int)blockDim.x) {
+    const int r = r0 + tid;
+    const bool in = r < a.R;
+    int len = in ? a.lens[r] : 0;
+    const int add_in = in ? a.new_lens[r] : 0;
+    len = len < 0 ? 0 : ((long long)len > room ? (int)room : len);
+    const bool gone = add_in < 0;
+    const long long add = gone ? 0 : add_in;
+    const int held = (int)(((long long)len + P - 1) >> a.page_shift);
+    const bool fits = len + add <= room;
+    const int need = !gone && fits ? (int)((len + add + P - 1) >> a.page_shift) - held : 0;
+    // a table cannot name more pages than there are (lens of another table would say so)
+    const int back = gone ? (held < a.num_pages ? held : a.num_pages) : 0;
+    const Sums s = block_scan({add, (long long)need, (long long)back}, carry, s_wave);
+    const bool ok = !gone && (add == 0 || (fits && s.add <= a.max_tokens &&
+                                           (need == 0 || s.need <= count)));
+    if (in) {
+      PageRow row;
+      row.old = len;
+      row.pages = gone ? -1 - back : (ok ? need : 0);
+      // released pages go behind the free ones, new ones come from the head; both offsets are
+      // below 2^63 and only used where they are at most num_pages
+      row.first = gone ? (int)((head + (long long)count + s.back - back) % a.num_pages)
+                       : (ok ? (int)((head + s.need - need) % a.num_pages) : 0);
+      row.ok = ok;
+      if (ok && need > 0) atomicMax(&s_taken, (int)s.need);
+      a.lens_out[r] = gone ? 0 : (ok ? (int)(len + add) : len);
+      a.status[r] = gone ? FADKV_ROW_RELEASED : (ok ? FADKV_ROW_OK : FADKV_ROW_REFUSED);
+      const int end = (int)(s.add < a.max_tokens ? s.add : a.max_tokens);
+      a.cu[r + 1] = end;
+      if constexpr (ONE) {
+        s_cu[r + 1] = end;
+        s_row[r] = row;
+      } else {
+        a.rows[r] = row;
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    const int taken = s_taken;
+    a.ring_state_out[0] = (int)((head + (long long)taken) % a.num_pages);
+    const long long left = (long long)count - taken + carry.back;
+    a.ring_state_out[1] = (int)(left > a.num_pages ? a.num_pages : left);
+  }
+  if constexpr (ONE) {
+    for (int j = tid; j < a.max_tokens; j += (int)blockDim.x) {
+      const bool in = j < s_cu[a.R];
+      const int r = in ? row_of(s_cu, a.R, j) : 0;
+      fill_token(a, j, r, in, s_cu[r], s_row[r]);
+    }
+    for (int r = tid >> 6; r < a.R; r += (int)(blockDim.x >> 6)) fill_pages(a, r, s_row[r], tid & 63);
+  }
+}
+
+// workgroups [0, token_blocks): FILL_TOKENS tokens each; the others: a row per wave
+__global__ __launch_bounds__(FILL_THREADS) void pages_fill_kernel(PagesArgs a, int token_blocks) {
+  __shared__ int s_cu[MAX_ROWS + 1];
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= token_blocks) {
+    const int r = ((int)blockIdx.x - token_blocks) * (FILL_THREADS / 64) + (tid >> 6);
+    if (r < a.R) fill_pages(a, r, a.rows[r], tid & 63);
+    return;
+  }
+  for (int r = tid; r <= a.R; r += FILL_THREADS) s_cu[r] = a.cu[r];
+  __syncthreads();
+  const int j0 = (int)blockIdx.x * FILL_TOKENS;
+#pragma unroll
+  for (int k = 0; k < FILL_TOKENS / FILL_THREADS; ++k) {
+    const int j = j0 + k * FILL_THREADS + tid;
+    if (j >= a.max_tokens) break;
+    const bool in = j < s_cu[a.R];
+    const int r = in ? row_of(s_cu, a.R, j) : 0;
+    PageRow row = {0, 0, 0, 0};
+    if (in) row = a.rows[r];
+    fill_token(a, j, r, in, s_cu[r], row);
+  }
+}
+
+hipError_t launch_pages_advance(const PagesArgs &a, hipStream_t stream) {
+  if (a.R <= ONE_ROWS && a.max_tokens <= ONE_TOKENS) {
+    const int most = a.R > a.max_tokens ? a.R : a.max_tokens;
+    const int threads = most <= 64 ? 64 : (most <= 256 ? 256 : SCAN_THREADS);
+    hipLaunchKernelGGL(pages_scan_kernel<true>, dim3(1), dim3(threads), 0, stream, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(pages_scan_kernel<false>, dim3(1), dim3(SCAN_THREADS), 0, stream, a);
+  const int token_blocks = (int)(((int64_t)a.max_tokens + FILL_TOKENS - 1) / FILL_TOKENS);
+  const int row_blocks = (a.R + FILL_THREADS / 64 - 1) / (FILL_THREADS / 64);
+  if (token_blocks + row_blocks > 0)
+    hipLaunchKernelGGL(pages_fill_kernel, dim3((unsigned)(token_blocks + row_blocks)),
+                       dim3(FILL_THREADS), 0, stream, a, token_blocks);
+  return hipGetLastError();
+}
+
+}  // namespace fadkv

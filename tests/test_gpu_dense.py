@@ -1,0 +1,642 @@
+"""GPU parity of the paged dense cache against the 64-bit oracle (oracle/dense_oracle.py).
+
+Bookkeeping is exact.  Tolerances elsewhere count roundings, u = 2^-24 in fp32 and half a step of
+the output type (eps / 2) once at the end:
+* norm and rotation: the mean square's 12 additions count half in the root, then mean, eps, root,
+  reciprocal, two factors, cosine (its argument is rounded, pi u, and 2 u of its own), mscale, a
+  product and a sum: 20 u of |a| + |b|;
+* attention: a score is off by (d + 4) u sum|q k| scale and two more u of itself, p and the sum
+  each by that and 4 u, the running sums by (tokens / 32 + 64) u at most; p is rounded once more
+  to 16-bit types, in fp16 by 2^-25 of the largest p at least (its smallest numbers).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import dense_oracle
+from sparse_dictionary_coding_amd import fadkv, synth
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+TORCH = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+U = 2.0 ** -24
+
+
+def _half_step(dt):
+    return torch.finfo(dt).eps / 2
+
+
+def _f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _i32(a):
+    return torch.as_tensor(np.asarray(a), dtype=torch.int32, device=DEV)
+
+
+def _banner(msg):
+    print(f"[gpu-dense] {msg}", flush=True)
+
+
+# ---- bookkeeping --------------------------------------------------------------------------------
+def _advance_both(page, new, lens, table, ring, state, tokens, **kw):
+    ref = dense_oracle.pages_advance(page, new, lens, table, ring, state, tokens)
+    pt = fadkv.PageTable(_i32(table), _i32(lens), _i32(ring), _i32(state), page)
+    step = fadkv.fadkv_pages_advance(pt, _i32(new), tokens, **kw)
+    torch.cuda.synchronize()
+    got = {"table": pt.table, "ring": pt.ring, "lens": step.lens, "ring_state": step.ring_state,
+           "cu": step.cu, "status": step.status, "slots": step.slots, "positions": step.positions}
+    for name, t in got.items():
+        np.testing.assert_array_equal(t.cpu().numpy(), ref[name], err_msg=name)
+    return ref
+
+
+def _random_state(rng, page, R, width, spare):
+    lens = rng.integers(0, width * page + 1, R)
+    lens[rng.random(R) < 0.2] = 0
+    held = -(-lens // page)
+    num = int(held.sum()) + spare
+    ids = rng.permutation(num)
+    table = rng.integers(-5, num + 5, (R, width))
+    at = 0
+    for r in range(R):
+        table[r, :held[r]] = ids[at:at + held[r]]
+        at += held[r]
+    head = int(rng.integers(0, num))
+    ring = rng.integers(0, num, num)
+    for i, p in enumerate(ids[at:]):
+        ring[(head + i) % num] = p
+    return lens, table, ring, [head, num - at]
+
+
+@pytest.mark.parametrize("page,R,width,spare,most,share", [
+    (16, 1, 1, 1, 1, 1.0), (16, 64, 40, 30, 1, 1.0), (16, 65, 9, 70, 33, 1.2), (32, 300, 7, 200, 50, 1.0),
+    (256, 7, 5, 3, 700, 0.7), (64, 1024, 4, 400, 3, 1.1), (128, 1025, 3, 500, 90, 1.0),
+    (16, 8192, 3, 4000, 9, 0.9), (16, 3, 600, 2000, 9000, 1.0)])
+def test_pages_advance(page, R, width, spare, most, share):
+    """Ragged batches with released, idle and refused rows; `share`: slots given of those wanted."""
+    _banner(f"pages R={R} page={page}")
+    rng = np.random.default_rng(R + page)
+    lens, table, ring, state = _random_state(rng, page, R, width, spare)
+    new = rng.integers(0, most + 1, R)
+    new[rng.random(R) < 0.1] = -1
+    tokens = int(np.maximum(new, 0).sum() * share) + 3
+    ref = _advance_both(page, new, lens, table, ring, state, tokens)
+    if R > 60:
+        assert set(ref["status"]) == {0, 1, 2} or R in (64, 1024)
+
+
+def test_pages_advance_edges():
+    _banner("pages edges")
+    none = np.zeros((0, 4), int)
+    _advance_both(16, [], [], none, [3, 4], [1, 2], 5)                     # no rows: padding only
+    _advance_both(16, [-1, 0], [0, 0], [[-1], [-1]], [0], [0, 1], 0)       # nothing moves
+    _advance_both(16, [1, 1], [16, 16], [[0, -1], [1, -1]], [2, 0, 1], [0, 1], 2)   # pool ends
+    _advance_both(16, [17, 1], [0, 0], [[-1], [-1]], [0, 1], [1, 2], 18)   # row outgrows its table
+    _advance_both(16, [5, 3, 0, -1], [1, 2, 3, 4], [[0], [1], [2], [3]], [0] * 4, [2, 0], 6)
+    _advance_both(16, [(1 << 31) - 1, 1, (1 << 31) - 1], [0, 0, 5], [[-1], [-1], [0]], [0, 1, 2],
+                  [1, 2], 4)                                               # sums past 32 bits
+    # lengths outside the table count as its ends
+    ref = dense_oracle.pages_advance(16, [0, 0], [99, -4], [[0, 1], [2, 3]], [0] * 4, [0, 0], 1)
+    pt = fadkv.PageTable(_i32([[0, 1], [2, 3]]), _i32([99, -4]), _i32([0] * 4), _i32([0, 0]), 16)
+    step = fadkv.fadkv_pages_advance(pt, _i32([0, 0]), 1)
+    assert step.lens.tolist() == ref["lens"].tolist() == [32, 0]
+
+
+def test_pages_advance_many_steps_reuse_every_page():
+    """Rows grow, end and start again for many steps, in place; no page is ever held twice."""
+    _banner("pages long run")
+    page, R, width, num = 16, 40, 6, 150
+    rng = np.random.default_rng(5)
+    pt = fadkv.PageTable.empty(R, width, num, page, DEV)
+    step = fadkv.PageStep.empty(pt, 2000, in_place=True)
+    state = (np.zeros(R, int), np.full((R, width), -1), np.arange(num), [0, num])
+    seen = set()
+    for _ in range(60):
+        new = rng.integers(0, 30, R)
+        new[rng.random(R) < 0.15] = -1
+        ref = dense_oracle.pages_advance(page, new, state[0], state[1], state[2], state[3], 2000)
+        state = (ref["lens"], ref["table"], ref["ring"], ref["ring_state"])
+        fadkv.fadkv_pages_advance(pt, _i32(new), out=step)
+        assert pt.lens.tolist() == ref["lens"].tolist()
+        assert pt.ring_state.tolist() == list(ref["ring_state"])
+        assert step.slots.tolist() == ref["slots"].tolist()
+        table = pt.table.tolist()
+        held = [table[r][i] for r in range(R) for i in range(-(-int(ref["lens"][r]) // page))]
+        assert len(set(held)) == len(held) and int(ref["ring_state"][1]) == num - len(held)
+        seen |= set(ref["status"])
+    assert seen == {0, 1, 2}
+
+
+# ---- norm and rotation --------------------------------------------------------------------------
+def _heads_case(dt, n, heads, kv, d, norm, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    qkv = torch.randn(n, heads + 2 * kv, d, generator=g).to(TORCH[dt])
+    w = [(1 + 0.3 * torch.randn(d, generator=g)).to(TORCH[dt]) if norm else None for _ in range(2)]
+    return qkv, w[0], w[1]
+
+
+def _close(got, ref, size, dt, roundings=20):
+    tol = _half_step(dt) * np.abs(ref) * (1 + 2.0 ** -7) + roundings * U * size
+    if dt == torch.float16:
+        tol = tol + 2.0 ** -25
+    err = np.abs(_f64(got) - ref)
+    assert (err <= tol).all(), (err - tol).max()
+
+
+NR = [
+    # dtype, n, heads, kv, d, rot, interleaved, norm, mscale, first position
+    ("bf16", 5, 4, 2, 128, 128, False, True, 1.0, 0),
+    ("f16", 17, 3, 1, 64, 64, True, False, 1.0, 131071),
+    ("f32", 9, 5, 5, 128, 96, False, True, 1.25, 1000003),
+    ("f32", 4, 1, 1, 64, 16, True, True, 0.5, (1 << 30) + 7),
+    ("bf16", 1, 32, 8, 128, 32, True, True, 1.0, 8191),
+    ("f16", 3, 2, 1, 128, 0, False, True, 1.0, 0),
+    ("f32", 1030, 2, 1, 64, 48, False, False, 1.0, 3),       # four tokens a workgroup, odd end
+    ("bf16", 1027, 6, 2, 128, 128, True, True, 1.0, 50),
+    ("f16", 2, 65, 13, 64, 32, False, True, 1.0, 77),
+]
+
+
+@pytest.mark.parametrize("dt,n,heads,kv,d,rot,inter,norm,mscale,first", NR)
+def test_norm_rope(dt, n, heads, kv, d, rot, inter, norm, mscale, first):
+    _banner(f"norm_rope {dt} n={n} heads={heads}/{kv} d={d} rot={rot}")
+    qkv, qw, kw = _heads_case(dt, n, heads, kv, d, norm, seed=n + d)
+    rng = np.random.default_rng(n)
+    freqs = fadkv.fadkv_rope_freqs(rot, 500000.0, device="cpu")[0] if rot else None
+    pos = first + np.arange(n)
+    pos[rng.random(n) < 0.15] = -1
+    page = 16
+    num = -(-n // page) + 2
+    slots = rng.permutation(num * page)[:n]
+    slots[rng.random(n) < 0.1] = -1
+    if n > 2:
+        slots[0], slots[1], pos[2] = num * page, -(1 << 31), first     # outside: not written
+    x = qkv.to(DEV)
+    q, k, v = x[:, :heads], x[:, heads:heads + kv], x[:, heads + kv:]
+    pages = fadkv.Pages.empty(num, kv, page, d, TORCH[dt], DEV)
+    for t in (pages.k, pages.v):
+        t.fill_(7.0)
+    rows = [torch.full((kv, n, d), 5.0, dtype=TORCH[dt], device=DEV) for _ in range(2)]
+    out = torch.full((n, heads, d), 3.0, dtype=TORCH[dt], device=DEV)
+    dev = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    got = fadkv.fadkv_norm_rope(q, k, v, _i32(pos), dev(freqs), dev(qw), dev(kw), 1e-5, inter, mscale,
+                                pages, _i32(slots), out, rows[0], rows[1])
+    torch.cuda.synchronize()
+    assert got is out
+    f = None if freqs is None else freqs.numpy()
+    w64 = [None if w is None else _f64(w) for w in (qw, kw)]
+    qr, qs = dense_oracle.norm_rope(_f64(qkv[:, :heads]), w64[0], pos, f, np.float32(1e-5), inter, mscale)
+    kr, ks = dense_oracle.norm_rope(_f64(qkv[:, heads:heads + kv]), w64[1], pos, f, np.float32(1e-5),
+                                    inter, mscale)
+    real = pos >= 0
+    _close(out[torch.as_tensor(real).to(DEV)], qr[real], qs[real], TORCH[dt])
+    assert (out[torch.as_tensor(~real).to(DEV)] == 3.0).all()
+    vt = v.transpose(0, 1)
+    rt = torch.as_tensor(real).to(DEV)
+    _close(rows[0][:, rt].transpose(0, 1), kr[real], ks[real], TORCH[dt])
+    assert torch.equal(rows[1][:, rt], vt[:, rt])
+    assert (rows[0][:, ~rt] == 5.0).all() and (rows[1][:, ~rt] == 5.0).all()
+    # what is in the pages is the rows, bit for bit, and nothing else changed
+    want_k, want_v = torch.full_like(pages.k, 7.0), torch.full_like(pages.v, 7.0)
+    for i in range(n):
+        s = int(slots[i])
+        if real[i] and 0 <= s < num * page:
+            want_k[s // page, :, s % page] = rows[0][:, i]
+            want_v[s // page, :, s % page] = v[i]
+    assert torch.equal(pages.k, want_k) and torch.equal(pages.v, want_v)
+
+
+def test_norm_rope_in_place_without_pages_and_empty():
+    _banner("norm_rope in place")
+    qkv, qw, kw = _heads_case("bf16", 6, 3, 3, 64, True)
+    x = qkv.to(DEV)
+    q, k, v = (x[:, 3 * i:3 * i + 3].contiguous() for i in range(3))
+    freqs, _ = fadkv.fadkv_rope_freqs(64, 10000.0, device=DEV)
+    pos = _i32(np.arange(6))
+    ref = fadkv.fadkv_norm_rope(q, k, v, pos, freqs, qw.to(DEV), kw.to(DEV))
+    q2 = q.clone()
+    assert fadkv.fadkv_norm_rope(q2, k, v, pos, freqs, qw.to(DEV), kw.to(DEV), q_out=q2) is q2
+    assert torch.equal(ref, q2)
+    e = torch.empty(0, 3, 64, dtype=torch.bfloat16, device=DEV)
+    assert fadkv.fadkv_norm_rope(e, e, e, _i32([]), freqs).shape == (0, 3, 64)
+    # one token whose stride says nothing, zero and non-finite heads
+    one = torch.zeros(1, 3, 64, dtype=torch.bfloat16, device=DEV)
+    one[0, 1, 5] = float("nan")
+    y = fadkv.fadkv_norm_rope(one, k[:1], v[:1], pos[:1], freqs, qw.to(DEV), kw.to(DEV))
+    assert (y[0, 0] == 0).all() and y[0, 1].isnan().all() and (y[0, 2] == 0).all()
+
+
+# ---- attention ----------------------------------------------------------------------------------
+def _cache(dt, kv, d, page, lens, width=None, seed=0, spare=3, junk=float("nan")):
+    """Pages in random order holding lens[r] tokens of each row; everything else is `junk`."""
+    g = torch.Generator().manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    lens = np.asarray(lens)
+    held = -(-lens // page)
+    num = int(held.sum()) + spare
+    width = max(1, int(held.max())) + 1 if width is None else width
+    ids = rng.permutation(num)
+    table = rng.choice([-1, num, 1 << 30, -(1 << 31)], (len(lens), width))
+    k, v = (torch.full((num, kv, page, d), junk) for _ in range(2))
+    at = 0
+    for r, n in enumerate(lens):
+        for i in range(held[r]):
+            here = min(page, n - i * page)
+            table[r, i] = ids[at]
+            k[ids[at], :, :here] = torch.randn(kv, here, d, generator=g)
+            v[ids[at], :, :here] = torch.randn(kv, here, d, generator=g)
+            at += 1
+    return fadkv.Pages(k.to(TORCH[dt]).to(DEV), v.to(TORCH[dt]).to(DEV)), _i32(table)
+
+
+def _gathered(pages, table, r, tokens):
+    """K, V [tokens][kv][d] in 64 bits and which tokens have a valid page."""
+    page = pages.page_size
+    K, V = np.zeros((tokens, *pages.k.shape[1::2])), np.zeros((tokens, *pages.k.shape[1::2]))
+    there = np.zeros(tokens, bool)
+    ids = table[r].tolist()
+    for i in range(-(-tokens // page)):
+        if 0 <= ids[i] < pages.k.shape[0]:
+            n = min(page, tokens - i * page)
+            K[i * page:i * page + n] = _f64(pages.k[ids[i], :, :n]).transpose(1, 0, 2)
+            V[i * page:i * page + n] = _f64(pages.v[ids[i], :, :n]).transpose(1, 0, 2)
+            there[i * page:i * page + n] = True
+    return K, V, there
+
+
+def _check_query(got, q, pos, K, V, there, scale, window, sinks, dt, what):
+    ref, size, top, raw = dense_oracle.attend_query(q, pos, K, V, there, scale, window, sinks)
+    d = q.shape[0]
+    e = 2 * ((d + 4) * raw + 4 * top + 4) * U + (K.shape[0] / 32 + 64) * U
+    u = _half_step(dt)
+    tol = u * np.abs(ref) * 1.01 + e * size
+    if dt != torch.float32:
+        tol = tol + u * size
+    if dt == torch.float16:
+        tol = tol + 2.0 ** -25 * np.abs(V).sum(0) + 2.0 ** -25
+    err = np.abs(got - ref)
+    assert (err <= tol).all(), (what, err.max(), tol.min())
+
+
+def _check_paged(dt, kv, group, d, page, lens, window=0, sinks=0, seed=0, spoil=None, max_len=None, **kw):
+    pages, table = _cache(dt, kv, d, page, lens, seed=seed)
+    if spoil:
+        spoil(pages, table)
+    g = torch.Generator().manual_seed(seed + 1)
+    q = (2 * torch.randn(len(lens), kv * group, d, generator=g)).to(TORCH[dt])
+    scale = d ** -0.5
+    out = fadkv.fadkv_attend_paged(pages, table, _i32(lens), q.to(DEV), scale, window, sinks, max_len, **kw)
+    torch.cuda.synchronize()
+    got = _f64(out)
+    assert np.isfinite(got).all()
+    for r, n in enumerate(lens):
+        K, V, there = _gathered(pages, table, r, n)
+        for h in range(kv * group):
+            _check_query(got[r, h], _f64(q[r, h]), n - 1, K[:, h // group], V[:, h // group], there,
+                         scale, window, sinks, TORCH[dt], (r, n, h))
+    return out
+
+
+PAGED = [
+    # dtype, kv heads, group, d, page, lens, window, sinks
+    ("f16", 2, 3, 128, 16, [1, 15, 16, 17, 31, 32, 33, 0, 300], 0, 0),
+    ("bf16", 1, 4, 64, 32, [257, 1, 64, 0], 0, 0),
+    ("f32", 2, 5, 128, 16, [100, 7, 1], 0, 0),
+    ("f32", 1, 1, 64, 256, [600, 256, 255], 0, 0),
+    ("bf16", 8, 4, 128, 64, [2000], 0, 0),                       # one row: split over its length
+    ("f16", 1, 16, 64, 128, [1111, 3], 0, 0),
+    ("bf16", 1, 17, 128, 16, [90, 40], 0, 0),                    # two blocks of query heads
+    ("f16", 1, 64, 64, 16, [50], 0, 0),
+    ("bf16", 2, 2, 128, 16, [500, 100, 64, 33, 1, 0], 64, 0),
+    ("f16", 2, 4, 64, 16, [999, 130, 40, 5], 33, 4),             # gap, touching, all visible
+    ("f32", 3, 1, 128, 32, [700, 65], 1, 1),
+    ("bf16", 1, 8, 64, 16, [400, 80], 16, 100),                  # more first tokens than a tile
+    ("f16", 1, 1, 128, 16, [3000], 100, 40),
+]
+
+
+@pytest.mark.parametrize("dt,kv,group,d,page,lens,window,sinks", PAGED)
+def test_attend_paged(dt, kv, group, d, page, lens, window, sinks):
+    _banner(f"paged {dt} kv={kv}x{group} d={d} page={page} lens={lens} window={window}/{sinks}")
+    out = _check_paged(dt, kv, group, d, page, lens, window, sinks, seed=page + d)
+    for r, n in enumerate(lens):
+        if n == 0:
+            assert (out[r] == 0).all()
+
+
+def test_attend_paged_any_length_bound_is_right():
+    """max_len only sizes the split: too small, exact and the whole table."""
+    for bound in (1, 700, 33 * 16):
+        _banner(f"paged max_len={bound}")
+        _check_paged("f16", 1, 4, 128, 16, [700, 513], seed=3, max_len=min(bound, 45 * 16))
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_attend_paged_pages_that_are_not_there(dt):
+    """Ids outside the pool hide their tokens, wherever they stand; lens past the table end there."""
+    _banner(f"paged bad pages {dt}")
+
+    def spoil(pages, table):
+        table[0, 0], table[0, 3], table[1, 1] = -1, pages.k.shape[0], 1 << 30
+        table[2] = -7
+    out = _check_paged(dt, 2, 2, 64, 16, [100, 50, 40], spoil=spoil)
+    assert (out[2] == 0).all()
+    pages, table = _cache(dt, 1, 64, 16, [48], width=3)
+    q = torch.randn(1, 2, 64, device=DEV).to(TORCH[dt])
+    a, b, c = (fadkv.fadkv_attend_paged(pages, table, _i32([n]), q, 0.1) for n in (48, 1000, -5))
+    assert torch.equal(a, b) and (c == 0).all()
+
+
+def test_attend_paged_large_scores_and_infinities():
+    _banner("paged large scores")
+    pages, table = _cache("f32", 1, 64, 16, [40])
+    q = torch.randn(1, 1, 64, device=DEV)
+    out = fadkv.fadkv_attend_paged(pages, table, _i32([40]), q, 1e4)       # one weight is 1
+    K, V, there = _gathered(pages, table, 0, 40)
+    best = int(np.argmax(K[:, 0] @ _f64(q[0, 0])))
+    np.testing.assert_allclose(_f64(out[0, 0]), V[best, 0], rtol=1e-5, atol=1e-6)
+    pages.v[int(table[0, 0]), 0, 2] = float("inf")
+    assert fadkv.fadkv_attend_paged(pages, table, _i32([40]), q, 0.1).isinf().all()
+    pages.k[int(table[0, 0]), 0, 2] = float("nan")
+    assert fadkv.fadkv_attend_paged(pages, table, _i32([40]), q, 0.1).isnan().all()
+    # a row that does not see token 2 is untouched by it
+    a = fadkv.fadkv_attend_paged(pages, table, _i32([40]), q, 0.1, window=30)
+    assert a.isfinite().all()
+
+
+def test_attend_paged_beyond_32_bits():
+    """Pages whose elements lie past 2^31 and bytes past 2^33."""
+    _banner("paged past 32 bits")
+    num, kv, page, d = 17000, 8, 256, 128                                  # 8.9 GB each
+    pages = fadkv.Pages.empty(num, kv, page, d, torch.float16, DEV)
+    ids = [16999, 8191, 8192, 0, 16384]
+    for p in ids:
+        pages.k[p].normal_()
+        pages.v[p].normal_()
+    table, n = _i32([ids]), 5 * page - 3
+    q = torch.randn(1, kv, d, device=DEV).half()
+    out = fadkv.fadkv_attend_paged(pages, table, _i32([n]), q, d ** -0.5)
+    pr = fadkv.fadkv_attend_prompt(pages, table, _i32([n]), _i32([0, 1]), q, d ** -0.5)
+    K, V, there = _gathered(pages, table, 0, n)
+    for h in range(kv):
+        for o in (out, pr):
+            _check_query(_f64(o[0, h]), _f64(q[0, h]), n - 1, K[:, h], V[:, h], there, d ** -0.5, 0, 0,
+                         torch.float16, h)
+    kvs = torch.randn(1, kv, d, device=DEV).half()
+    fadkv.fadkv_norm_rope(q, kvs, kvs, _i32([5]), None, pages=pages, slots=_i32([16999 * page + 255]))
+    assert torch.equal(pages.k[16999, :, 255], kvs[0]) and torch.equal(pages.v[16999, :, 255], kvs[0])
+
+
+def _check_prompt(dt, kv, group, d, page, cached, fresh, window=0, sinks=0, seed=0, pad=0, rows=None):
+    lens = np.asarray(cached) + np.asarray(fresh)
+    pages, table = _cache(dt, kv, d, page, lens, seed=seed)
+    cu = np.concatenate([[0], np.cumsum(fresh)])
+    n = int(cu[-1])
+    g = torch.Generator().manual_seed(seed + 1)
+    q = (2 * torch.randn(n + pad, kv * group, d, generator=g)).to(TORCH[dt])
+    out = torch.full(q.shape, 9.0, dtype=TORCH[dt], device=DEV)
+    scale = d ** -0.5
+    fadkv.fadkv_attend_prompt(pages, table, _i32(lens), _i32(cu), q.to(DEV), scale, window, sinks, out)
+    torch.cuda.synchronize()
+    got = _f64(out)
+    assert (got[n:] == 9.0).all()
+    assert np.isfinite(got).all()
+    rng = np.random.default_rng(seed)
+    for r in range(len(lens)):
+        K, V, there = _gathered(pages, table, r, int(lens[r]))
+        at = range(fresh[r])
+        if fresh[r] > 12:      # the ends and a sample of the rest
+            at = sorted({0, 1, fresh[r] - 1, *rng.choice(fresh[r], 9, replace=False)})
+        for i in at:
+            for h in range(kv * group):
+                _check_query(got[cu[r] + i, h], _f64(q[cu[r] + i, h]), cached[r] + i, K[:, h // group],
+                             V[:, h // group], there, scale, window, sinks, TORCH[dt], (r, i, h))
+
+
+PROMPT = [
+    # dtype, kv heads, group, d, page, cached, fresh, window, sinks, padding
+    ("bf16", 2, 4, 128, 16, [0, 0, 0], [1, 16, 37], 0, 0, 5),
+    ("f16", 1, 3, 64, 32, [0, 100, 7], [200, 1, 0], 0, 0, 0),
+    ("f32", 2, 2, 128, 16, [0, 33], [50, 3], 0, 0, 2),
+    ("f32", 1, 5, 64, 64, [70], [129], 20, 3, 0),
+    ("bf16", 1, 1, 64, 16, [0], [300], 0, 0, 0),
+    ("bf16", 1, 8, 128, 16, [0, 500], [150, 40], 64, 4, 1),
+    ("f16", 2, 1, 128, 128, [1000], [65], 1, 0, 0),
+    ("f16", 1, 2, 64, 16, [10, 0], [400, 90], 17, 70, 0),
+    ("bf16", 1, 64, 64, 16, [3], [5], 0, 0, 0),
+    ("f16", 1, 7, 128, 16, [0, 0, 0, 0, 0], [0, 2, 0, 9, 0], 0, 0, 3),
+    ("bf16", 3, 5, 128, 256, [255, 1], [258, 257], 100, 30, 0),
+]
+
+
+@pytest.mark.parametrize("dt,kv,group,d,page,cached,fresh,window,sinks,pad", PROMPT)
+def test_attend_prompt(dt, kv, group, d, page, cached, fresh, window, sinks, pad):
+    _banner(f"prompt {dt} kv={kv}x{group} d={d} page={page} {cached}+{fresh} window={window}/{sinks}")
+    _check_prompt(dt, kv, group, d, page, cached, fresh, window, sinks, seed=d + page, pad=pad)
+
+
+def test_attend_prompt_many_rows():
+    """More rows than a wave scans at once, most of them single tokens or empty."""
+    _banner("prompt many rows")
+    rng = np.random.default_rng(9)
+    fresh = rng.choice([0, 1, 1, 2, 40], 150).tolist()
+    _check_prompt("f16", 1, 2, 64, 16, rng.integers(0, 60, 150).tolist(), fresh, pad=4)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attend_prompt_queries_before_the_cache(dt):
+    """More new tokens than the row holds (a refused row): what lies before it sees nothing."""
+    _banner(f"prompt refused row {dt}")
+    pages, table = _cache(dt, 1, 64, 16, [20])
+    q = torch.randn(50, 2, 64, device=DEV).to(TORCH[dt])
+    out = fadkv.fadkv_attend_prompt(pages, table, _i32([20]), _i32([0, 50]), q, 0.125)
+    assert (out[:30] == 0).all() and out.isfinite().all()
+    ref = fadkv.fadkv_attend_prompt(pages, table, _i32([20]), _i32([0, 20]), q[30:].contiguous(), 0.125)
+    torch.testing.assert_close(out[30:], ref, rtol=0, atol=0 if dt == "f32" else 0.02)
+    # offsets that run past the batch are cut at its end, missing pages hide their tokens
+    cut = fadkv.fadkv_attend_prompt(pages, table, _i32([20]), _i32([30, 999]), q, 0.125,
+                                    out=torch.zeros_like(q))
+    assert (cut[:30] == 0).all() and cut.isfinite().all()
+    table[0] = -1
+    assert (fadkv.fadkv_attend_prompt(pages, table, _i32([20]), _i32([0, 50]), q, 0.125) == 0).all()
+
+
+def test_prompt_and_token_forms_agree():
+    """The last query of a prompt and the same query as a single token."""
+    _banner("prompt against token")
+    pages, table = _cache("bf16", 2, 128, 16, [333, 90])
+    q = torch.randn(423, 8, 128, device=DEV).bfloat16()
+    for window, sinks in ((0, 0), (50, 4)):
+        p = fadkv.fadkv_attend_prompt(pages, table, _i32([333, 90]), _i32([0, 333, 423]), q, 0.1, window, sinks)
+        t = fadkv.fadkv_attend_paged(pages, table, _i32([333, 90]), q[[332, 422]], 0.1, window, sinks)
+        torch.testing.assert_close(p[[332, 422]].float(), t.float(), rtol=2.0 ** -6, atol=2.0 ** -8)
+
+
+# ---- together -----------------------------------------------------------------------------------
+def _model_layer(seed, rows, heads, kv, d, dt):
+    g = torch.Generator().manual_seed(seed)
+    w = [(1 + 0.2 * torch.randn(d, generator=g)).to(dt).to(DEV) for _ in range(2)]
+    freqs, m = fadkv.fadkv_rope_freqs(d, 500000.0, "bands", 8.0, 1.0, 4.0, 8192, device=DEV)
+    return w, freqs, m
+
+
+def test_decode_loop_of_one_layer():
+    """Prompts enter, then single tokens: lengths -> slots -> heads into the pages -> attention, with
+    a captured decode step replayed; every output against attention over all keys seen so far,
+    and the keys' rows go through the encoder."""
+    _banner("one layer's loop")
+    rows, heads, kv, d, page = 3, 8, 2, 64, 16
+    dt = torch.float16
+    (qw, kw), freqs, mscale = _model_layer(0, rows, heads, kv, d, dt)
+    pt = fadkv.PageTable.empty(rows, 12, 40, page, DEV)
+    pages = fadkv.Pages.empty(40, kv, page, d, dt, DEV)
+    g = torch.Generator().manual_seed(1)
+    keys, values = [[] for _ in range(rows)], [[] for _ in range(rows)]
+
+    def step(qkv, new, bufs, attend):
+        fadkv.fadkv_pages_advance(pt, new, out=bufs["step"])
+        s = bufs["step"]
+        fadkv.fadkv_norm_rope(qkv[:, :heads], qkv[:, heads:heads + kv], qkv[:, heads + kv:], s.positions,
+                              freqs, qw, kw, mscale=mscale, pages=pages, slots=s.slots, q_out=bufs["q"],
+                              k_rows=bufs["k"], v_rows=bufs["v"])
+        if attend == "prompt":
+            return fadkv.fadkv_attend_prompt(pages, pt.table, pt.lens, s.cu, bufs["q"], d ** -0.5, 40, 4,
+                                             out=bufs["out"])
+        return fadkv.fadkv_attend_paged(pages, pt.table, pt.lens, bufs["q"], d ** -0.5, 40, 4,
+                                        out=bufs["out"], workspace=bufs["ws"])
+
+    def buffers(n):
+        e = lambda *s: torch.zeros(*s, dtype=dt, device=DEV)  # noqa: E731
+        need = fadkv.fadkv_attend_paged_workspace_bytes(pages, rows, heads, 12 * page)
+        return {"step": fadkv.PageStep.empty(pt, n, in_place=True), "q": e(n, heads, d), "k": e(kv, n, d),
+                "v": e(kv, n, d), "out": e(n, heads, d),
+                "ws": torch.empty(max(need, 1), dtype=torch.uint8, device=DEV)}
+
+    def check(bufs, fresh):
+        at = 0
+        out, q = _f64(bufs["out"]), _f64(bufs["q"])
+        for r, f in enumerate(fresh):
+            for i in range(f):
+                keys[r].append(_f64(bufs["k"][:, at + i]))
+                values[r].append(_f64(bufs["v"][:, at + i]))
+            K, V = np.array(keys[r]), np.array(values[r])
+            for i in range(f):
+                pos = len(keys[r]) - f + i
+                for h in range(heads):
+                    _check_query(out[at + i, h], q[at + i, h], pos, K[:, h // 4], V[:, h // 4],
+                                 [True] * len(K), d ** -0.5, 40, 4, dt, (r, pos, h))
+            at += f
+
+    fresh = [70, 1, 33]
+    b = buffers(110)
+    step(torch.randn(110, heads + 2 * kv, d, generator=g).to(dt).to(DEV), _i32(fresh), b, "prompt")
+    torch.cuda.synchronize()
+    assert pt.lens.tolist() == fresh
+    check(b, fresh)
+
+    # the decode step, captured; every replay against the oracle, with eager work between them
+    b = buffers(rows)
+    x = torch.zeros(rows, heads + 2 * kv, d, dtype=dt, device=DEV)
+    one = _i32([1] * rows)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            step(x, one, b, "token")
+    torch.cuda.synchronize()
+    assert pt.lens.tolist() == fresh            # capturing runs nothing
+    for rep in range(20):
+        x.copy_(torch.randn(x.shape, generator=g).to(dt))
+        b["out"].fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert pt.lens.tolist() == [f + rep + 1 for f in fresh]
+        check(b, [1] * rows)
+
+    # the step's rows are the encoder's: keys of dictionary 0, values of dictionary 1
+    w = synth.WORKLOADS["tiny"]
+    atoms = torch.cat([synth.SyntheticKV(w).atoms()] * 2).to(dt).to(DEV)
+    X = torch.stack([b["k"].reshape(kv * rows, d), b["v"].reshape(kv * rows, d)])
+    codes = fadkv.fadkv_encode(atoms, X, fadkv.Params(n=32, s=4))
+    torch.cuda.synchronize()
+    assert codes.relerr.isfinite().all() and (codes.idx >= 0).all()
+
+
+def test_two_graphs_share_a_workspace_and_streams_do_not_mix():
+    """Two captured calls on one workspace, replayed in turn; and calls on other streams, with
+    workspaces of their own, at once."""
+    _banner("graphs and streams")
+    lens = [900, 700]
+    pages, table = _cache("f16", 2, 128, 16, lens)
+    g = torch.Generator().manual_seed(4)
+    qs = [torch.randn(2, 8, 128, generator=g).half().to(DEV) for _ in range(2)]
+    ref = [fadkv.fadkv_attend_paged(pages, table, _i32(lens), q, 0.1) for q in qs]
+    need = fadkv.fadkv_attend_paged_workspace_bytes(pages, 2, 8, table.shape[1] * 16)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    L = _i32(lens)
+    outs, graphs = [torch.empty_like(q) for q in qs], []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for q, o in zip(qs, outs):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=side):
+                fadkv.fadkv_attend_paged(pages, table, L, q, 0.1, out=o, workspace=ws)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        ws.fill_(0xFF)
+        for o in outs:
+            o.fill_(float("nan"))
+        for gr in graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, outs))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [fadkv.fadkv_attend_paged(pages, table, L, q, 0.1, stream=s if i else s.cuda_stream)
+           for i, (q, s) in enumerate(zip(qs, streams))]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+def test_binding_refusals():
+    _banner("binding refusals")
+    pages, table = _cache("f16", 1, 64, 16, [20])
+    L, q = _i32([20]), torch.randn(1, 2, 64, device=DEV).half()
+    ok = lambda **kw: fadkv.fadkv_attend_paged(**{**dict(pages=pages, table=table, lens=L, q=q, scale=0.1), **kw})  # noqa: E731
+    ok()
+    for err, kw in [(TypeError, dict(q=q.float())), (ValueError, dict(q=q[:, :, :32].contiguous())),
+                    (ValueError, dict(q=torch.cat([q, q]))), (ValueError, dict(q=q.cpu())),
+                    (TypeError, dict(table=table.long())), (ValueError, dict(table=table[0])),
+                    (ValueError, dict(lens=_i32([1, 2]))), (ValueError, dict(out=torch.empty(1, 3, 64, device=DEV).half())),
+                    (ValueError, dict(q=torch.randn(1, 64, 2, device=DEV).half().transpose(1, 2))),
+                    (ValueError, dict(q=q.clone().requires_grad_())),
+                    (fadkv.FadkvError, dict(window=-1)), (fadkv.FadkvError, dict(max_len=0)),
+                    (ValueError, dict(pages=fadkv.Pages(pages.k, pages.v[:, :, :, :32])))]:
+        with pytest.raises(err):
+            ok(**kw)
+    with torch.no_grad():
+        ok(q=q.clone().requires_grad_())
+    x = torch.randn(4, 6, 64, device=DEV).half()
+    args = (x[:, :2], x[:, 2:4], x[:, 4:], _i32(range(4)), None)
+    fadkv.fadkv_norm_rope(*args)
+    for err, kw in [(ValueError, dict(pages=pages)), (ValueError, dict(slots=_i32(range(4)))),
+                    (TypeError, dict(q_weight=torch.ones(64, device=DEV))),
+                    (ValueError, dict(k_rows=torch.empty(4, 2, 64, device=DEV).half())),
+                    (fadkv.FadkvError, dict(eps=-1.0))]:
+        with pytest.raises(err):
+            fadkv.fadkv_norm_rope(*args, **kw)
+    with pytest.raises(ValueError):
+        fadkv.fadkv_norm_rope(x.transpose(1, 2).contiguous().transpose(1, 2)[:, :2], *args[1:])
+    with pytest.raises(ValueError):
+        fadkv.fadkv_norm_rope(args[0], args[1], x[:, 4:5], *args[3:])
+    pt = fadkv.PageTable.empty(2, 4, 8, 16, DEV)
+    with pytest.raises(ValueError):
+        fadkv.fadkv_pages_advance(pt, _i32([1, 1]))
+    with pytest.raises(ValueError):
+        fadkv.fadkv_pages_advance(pt, _i32([1, 1, 1]), 3)
+    with pytest.raises(fadkv.FadkvError):
+        fadkv.fadkv_pages_advance(fadkv.PageTable.empty(2, 4, 8, 24, DEV), _i32([1, 1]), 3)
