@@ -1,9 +1,20 @@
 // Causal attention of packed prompt tokens over paged keys and values.
 //
 // A row's (token, query head of the group) pairs, token by token, are the columns: the `group` query
-// heads of a kv head share every key and value read.  A wave holds 16 columns and walks the
-// visible tiles of 32 tokens (attend_tile.h).
+// heads of a kv head share every key and value read.
+//
+// 16-bit types (attend_prompt_mfma_kernel): bound by the matrix cores, 4 d flops per column and
+// visible token.  A wave holds 32 columns, and the workgroup's four waves share tiles of 64 tokens
+// that come into LDS by direct copies, one tile ahead.  As in attend_tile.h the scores are
+// computed transposed (S^T = K Q^T, v_mfma_f32_32x32x16), so that a lane's p are its entries of the
+// second product's operand (O^T = V^T P^T) without leaving the lane, and V is read from LDS through
+// the transposing load.  The exponentials cost as many cycles as the products; what else the
+// vector unit does per score is kept to a maximum, a multiply-add, a sum and half a conversion:
+// O is rescaled only where a column's maximum grows by more than 2^8 (p stays below 2^8, which
+// fp32 sums and 16-bit p hold as well as p <= 1).
+// fp32 (attend_prompt_kernel): a wave holds 16 columns and walks tiles of 32 tokens in registers.
 #include "attend_tile.h"
+#include "tiles.h"
 
 namespace fadkv {
 
@@ -109,6 +120,301 @@ __global__ __launch_bounds__(64 * PR_WAVES) void attend_prompt_kernel(AttendArgs
   if (there) store_output<DT, D>(static_cast<uint8_t *>(a.out) + qi * T::ROWB, lane, x);
 }
 
+// ---- 16-bit types: LDS tiles of 64 tokens, v_mfma_f32_32x32x16 --------------------------------
+
+namespace {
+
+constexpr int PT = 64;   // tokens per tile
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+template <int DT>
+__device__ __forceinline__ void mfma32(const uint4 &a, const uint4 &b, float16_t &c) {
+  if constexpr (DT == DT_F16)
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a),
+                                               __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  else
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// Where the 16-byte chunk c of row r of a tile lies in its row.  Keys: a fragment read takes one
+// chunk of 16 rows, values: two 32-byte pieces of 4 rows; both then hit distinct banks.
+template <int D> __device__ __forceinline__ int key_swz(int r) {
+  return D == 128 ? (r & 15) : ((r >> 1) & 7);
+}
+template <int D> __device__ __forceinline__ int value_swz(int r) {
+  return D == 128 ? ((r & 3) << 1) : (((r >> 1) & 1) << 1);
+}
+
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+
+// workgroup barrier of LDS alone: the caller has waited for its own copies and LDS accesses
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+}  // namespace
+
+template <int DT, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(AttendArgs a) {
+  constexpr int ROWB = 2 * D;
+  constexpr int CPR = ROWB / 16;         // chunks per row
+  constexpr int NB = D / 32;             // 32-element blocks of d
+  constexpr int KC = D / 16;             // products per 32-token score block
+  constexpr int TILE = PT * ROWB;        // bytes of a K or V tile
+  constexpr int ROWS_W = PT / WAVES;     // rows of a tile that a wave copies
+  constexpr int LOADS = ROWS_W * ROWB / 1024;
+  static_assert(ROWS_W <= 16 && LOADS >= 1, "a wave copies rows of one 16-token group");
+  __shared__ __attribute__((aligned(256))) uint8_t s_kv[2][2][TILE];   // [stage][K, V]
+  __shared__ int s_miss[2][4];           // [stage][16-token group]: no valid page
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = lane & 31, h = lane >> 5;
+
+  const int head = (int)(blockIdx.x % a.kv_heads);
+  RowBlock rb = find_row(a, blockIdx.x / a.kv_heads, 32 * WAVES, lane);
+  if (rb.row >= a.R) return;
+  const int heads = a.kv_heads * a.group;
+  const int64_t cols = (int64_t)rb.tokens * a.group;
+  // the blocks with the most tokens first
+  rb.block = (int)((cols + 32 * WAVES - 1) / (32 * WAVES)) - 1 - rb.block;
+  const int64_t room = (int64_t)a.max_pages << a.page_shift;
+  int len = a.lens[rb.row];
+  len = len < 0 ? 0 : ((int64_t)len > room ? (int)room : len);
+  const int pos_first = len - rb.tokens;   // position of the row's first query
+
+  const int64_t b0 = (int64_t)rb.block * WAVES * 32;            // columns of the workgroup
+  const int64_t b1 = (b0 + 32 * WAVES < cols ? b0 + 32 * WAVES : cols) - 1;
+  const int64_t c0 = b0 + wave * 32;                            // and of the wave
+  const int64_t c1 = c0 + 31 < cols ? c0 + 31 : cols - 1;
+  const bool busy = c0 < cols;
+  const int64_t cc = c0 + col;
+  const bool there = cc < cols;
+  const int64_t ccl = there ? cc : cols - 1;
+  const int tok = (int)(ccl / a.group), gq = (int)(ccl % a.group);
+  const int pos = pos_first + tok;
+  const auto lo_of = [&](int p) { return a.window <= p ? p + 1 - a.window : 0; };
+  const Visible see = {lo_of(pos), pos + 1};
+  const int wg0 = pos_first + (int)(b0 / a.group), wg1 = pos_first + (int)(b1 / a.group);
+  const int w0 = pos_first + (int)((busy ? c0 : b0) / a.group);
+  const int w1 = pos_first + (int)((busy ? c1 : b1) / a.group);
+  const Visible any = {lo_of(wg0), wg1 + 1};                    // some column of the workgroup sees
+  const Visible some = {lo_of(w0), w1 + 1};                     // some column of the wave sees
+  const Visible all = {lo_of(w1), w0 + 1};                      // every column of the wave sees
+  const size_t qi = (size_t)(rb.begin + tok) * heads + (size_t)head * a.group + gq;
+
+  // queries: entry 8 h + j of product i is element 16 i + 8 h + j.  The score's sign goes into q, so
+  // that a column's largest score is its largest product.
+  const bool flat = __builtin_fabsf(a.scale) < 1e-37f;   // all scores 0
+  uint4 q[KC];
+  {
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) + qi * ROWB);
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+    const bool zero = !there || flat;
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+      const uint4 w = zero ? make_uint4(0, 0, 0, 0) : src[2 * i + h];
+      q[i] = make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
+    }
+  }
+  const float scale2 = flat ? 1.f : __builtin_fabsf(a.scale) * kLog2e;
+
+  PageView pv = {static_cast<const uint8_t *>(a.k), static_cast<const uint8_t *>(a.v),
+                 a.table + (size_t)rb.row * a.max_pages, a.num_pages, a.page_shift, a.kv_heads,
+                 head, a.max_pages};
+
+  // the visible tiles of the workgroup: [0, first) of the first tokens, then [from, last)
+  const int last = any.hi > 0 ? (any.hi + PT - 1) / PT : 0;
+  int first = ((a.sinks < any.hi ? a.sinks : (any.hi > 0 ? any.hi : 0)) + PT - 1) / PT;
+  int from = any.lo / PT;
+  if (first >= from) {
+    from = first > 0 ? 0 : from;
+    first = 0;
+  }
+  const int count = first + (last > from ? last - from : 0);
+  const auto start_of = [&](int i) { return (i < first ? i : from + i - first) * PT; };
+
+  // this wave's rows of a tile: ROWS_W of the 16-token group grp
+  const int grp = wave * ROWS_W / 16;
+  const int row0 = wave * ROWS_W;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&s_kv[0][0][0];
+  uint32_t koff[LOADS], voff[LOADS];
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) {
+    const int at = 64 * j + lane;
+    const int r = row0 + at / CPR, c = at % CPR;
+    koff[j] = (uint32_t)((r - grp * 16) * ROWB + (c ^ key_swz<D>(r)) * 16);
+    voff[j] = (uint32_t)((r - grp * 16) * ROWB + (c ^ value_swz<D>(r)) * 16);
+  }
+  const auto group_offset = [&](int i) -> int64_t {
+    return i < count ? group_at<ROWB>(pv, start_of(i) + grp * 16) : -1;
+  };
+  const auto issue = [&](int stage, int64_t at) {
+    if (at >= 0) {
+      const uint8_t *ks = tile::uniform_ptr(pv.k + at), *vs = tile::uniform_ptr(pv.v + at);
+      const uint32_t dst = lds0 + (uint32_t)stage * 2 * TILE + (uint32_t)row0 * ROWB;
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) {
+        tile::copy16_to_lds(ks, koff[j], dst + 1024u * j);
+        tile::copy16_to_lds(vs, voff[j], dst + TILE + 1024u * j);
+      }
+    }
+    if (lane == 0) s_miss[stage][grp] = at < 0;
+  };
+  // after the copies have landed: values that no column sees become zeros (p = 0 does not undo
+  // an infinity or NaN there)
+  const auto settle = [&](int i, int stage, int64_t at) {
+    tile::wait_vmem();
+    asm volatile("" ::: "memory");
+    const int t0 = start_of(i);
+    if (at < 0 || t0 + PT > any.hi || (t0 < any.lo && t0 + PT > a.sinks)) {
+      constexpr int LPR = 64 / ROWS_W;   // lanes per row
+      const int r = row0 + lane / LPR;
+      if (at < 0 || !sees(any, a.sinks, t0 + r)) {
+        uint4 *dst = reinterpret_cast<uint4 *>(&s_kv[stage][1][r * ROWB]);
+        for (int c = lane % LPR; c < CPR; c += LPR) dst[c] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    tile::wait_lds();
+  };
+
+  float16_t o[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[b][e] = 0.f;
+  float m = -__builtin_inff(), base = 0.f, l = 0.f;   // m in units of 1 / scale2
+
+  // the lane's byte offsets within a tile
+  int kaddr[2];
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) kaddr[kb] = (32 * kb + col) * ROWB;
+  const int kswz = key_swz<D>(col);   // the same for col + 32
+  // transposing read: lane 4 j + c of a 16-lane group gives key j's piece c, and gets element lane of
+  // the four keys.  Row r of block b of V^T is element D/2 ((r >> 2) & 1) + 16 b + 4 (r >> 3) +
+  // (r & 3), which leaves a lane with D/2 neighbouring elements of the output.
+  const int vkey = 4 * h + ((lane & 15) >> 2);
+  const int vr = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  const int vel = (D / 2) * ((vr >> 2) & 1) + 4 * (vr >> 3);     // element of block 0
+
+  int64_t at = group_offset(0);
+  if (count > 0) {
+    issue(0, at);
+    settle(0, 0, at);
+  }
+  int64_t at_next = group_offset(1);
+  lds_barrier();
+  for (int i = 0; i < count; ++i) {
+    const int stage = i & 1;
+    at = at_next;
+    if (i + 1 < count) issue(stage ^ 1, at);
+    at_next = group_offset(i + 2);
+    const int t0 = start_of(i);
+    const bool skip = !busy || t0 >= some.hi || (t0 + PT <= some.lo && t0 >= a.sinks);
+    if (!skip) {
+      const uint8_t *kt = s_kv[stage][0], *vt = s_kv[stage][1];
+      float16_t s[2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[kb][e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const uint4 ka = *reinterpret_cast<const uint4 *>(kt + kaddr[kb] + (((2 * c + h) ^ kswz) << 4));
+          mfma32<DT>(ka, q[c], s[kb]);
+        }
+      }
+      const int4 miss = *reinterpret_cast<const int4 *>(s_miss[stage]);
+      const bool full = !__builtin_amdgcn_readfirstlane(miss.x | miss.y | miss.z | miss.w) &&
+                        t0 + PT <= all.hi && (t0 >= all.lo || t0 + PT <= a.sinks);
+      if (!full) {
+        const int gone[4] = {miss.x, miss.y, miss.z, miss.w};
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int k = 32 * kb + 8 * (e >> 2) + (e & 3);   // + 4 h
+            if (gone[k >> 4] || !sees(see, a.sinks, t0 + k + 4 * h)) s[kb][e] = -__builtin_inff();
+          }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kb][e]);
+      if (__any(top * scale2 > m + 8.f)) {
+        top = fmaxf(top, other_half(top)) * scale2;
+        const float grown = fmaxf(m, top);
+        const float nb = grown == -__builtin_inff() ? 0.f : grown;
+        const float keep = __builtin_amdgcn_exp2f(m - nb);
+        m = grown;
+        base = nb;
+        l *= keep;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[b][e] *= keep;
+      }
+      uint4 p[4];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[e] = __builtin_amdgcn_exp2f(fmaf(s[kb][e], scale2, -base));
+          l += x[e];
+        }
+#pragma unroll
+        for (int g2 = 0; g2 < 2; ++g2)
+          p[2 * kb + g2] = make_uint4(round2<DT>(x[8 * g2], x[8 * g2 + 1]), round2<DT>(x[8 * g2 + 2], x[8 * g2 + 3]),
+                                      round2<DT>(x[8 * g2 + 4], x[8 * g2 + 5]), round2<DT>(x[8 * g2 + 6], x[8 * g2 + 7]));
+      }
+#pragma unroll
+      for (int g2 = 0; g2 < 4; ++g2) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint2 w[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int r = 16 * g2 + 8 * u + vkey;
+            const int el = vel + 16 * b;
+            const uint8_t *src = vt + r * ROWB + (((el >> 3) ^ value_swz<D>(vkey)) << 4) + ((el & 7) << 1);
+            w[u] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)src));
+          }
+          mfma32<DT>(make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), p[g2], o[b]);
+        }
+      }
+    }
+    if (i + 1 < count) settle(i + 1, stage ^ 1, at);
+    lds_barrier();
+  }
+  if (!there) return;
+  l += other_half(l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;   // no visible token: 0
+  uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + qi * ROWB + h * D);
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = o[b][8 * u + e] * inv;
+      dst[2 * b + u] = make_uint4(round2<DT>(x[0], x[1]), round2<DT>(x[2], x[3]),
+                                  round2<DT>(x[4], x[5]), round2<DT>(x[6], x[7]));
+    }
+}
+
+constexpr int PM_WAVES = 4;
+
+template <int DT, int D> static void attend_prompt_mfma_run(const AttendArgs &a, hipStream_t stream) {
+  const int64_t blocks = a.n * a.group / (32 * PM_WAVES) + (a.R < a.n ? a.R : a.n);
+  hipLaunchKernelGGL((attend_prompt_mfma_kernel<DT, D, PM_WAVES>),
+                     dim3((unsigned)(blocks * a.kv_heads)), dim3(64 * PM_WAVES), 0, stream, a);
+}
+
 template <int DT, int D> static void attend_prompt_run(const AttendArgs &a, hipStream_t stream) {
   // at most one started block more per row than the columns fill
   const int64_t blocks = a.n * a.group / (16 * PR_WAVES) + (a.R < a.n ? a.R : a.n);
@@ -121,11 +427,11 @@ hipError_t launch_attend_prompt(int dtype, int d, const AttendArgs &a, hipStream
     if (d == 64) attend_prompt_run<DT_F32, 64>(a, stream);
     else attend_prompt_run<DT_F32, 128>(a, stream);
   } else if (dtype == DT_F16) {
-    if (d == 64) attend_prompt_run<DT_F16, 64>(a, stream);
-    else attend_prompt_run<DT_F16, 128>(a, stream);
+    if (d == 64) attend_prompt_mfma_run<DT_F16, 64>(a, stream);
+    else attend_prompt_mfma_run<DT_F16, 128>(a, stream);
   } else {
-    if (d == 64) attend_prompt_run<DT_BF16, 64>(a, stream);
-    else attend_prompt_run<DT_BF16, 128>(a, stream);
+    if (d == 64) attend_prompt_mfma_run<DT_BF16, 64>(a, stream);
+    else attend_prompt_mfma_run<DT_BF16, 128>(a, stream);
   }
   return hipGetLastError();
 }
