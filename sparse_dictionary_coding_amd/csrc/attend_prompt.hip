@@ -50,11 +50,11 @@ __device__ __forceinline__ RowBlock find_row(const AttendArgs &a, int64_t blk, i
     through += before;
     const unsigned long long hit = __ballot(blk < through);
     if (hit) {
-      const int src = __builtin_ctzll(hit);
+      const int src = __builtin_ctzll(hit);   // the same for all lanes: scalar registers from here
       rb.row = r0 + src;
-      rb.block = (int)(blk - __shfl((long long)(through - mine), src, 64));
-      rb.begin = (int)__shfl((long long)b, src, 64);
-      rb.tokens = (int)__shfl((long long)(e - b), src, 64);
+      rb.block = __builtin_amdgcn_readlane((int)(blk - (through - mine)), src);
+      rb.begin = __builtin_amdgcn_readlane((int)b, src);
+      rb.tokens = __builtin_amdgcn_readlane((int)(e - b), src);
       return rb;
     }
     before = __shfl((long long)through, 63, 64);
@@ -171,7 +171,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   static_assert(ROWS_W <= 16 && LOADS >= 1, "a wave copies rows of one 16-token group");
   __shared__ __attribute__((aligned(256))) uint8_t s_kv[2][2][TILE];   // [stage][K, V]
   __shared__ int s_miss[2][4];           // [stage][16-token group]: no valid page
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, h = lane >> 5;
 
   const int head = (int)(blockIdx.x % a.kv_heads);
@@ -182,7 +183,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   // the blocks with the most tokens first
   rb.block = (int)((cols + 32 * WAVES - 1) / (32 * WAVES)) - 1 - rb.block;
   const int64_t room = (int64_t)a.max_pages << a.page_shift;
-  int len = a.lens[rb.row];
+  int len = __builtin_amdgcn_readfirstlane(a.lens[rb.row]);
   len = len < 0 ? 0 : ((int64_t)len > room ? (int)room : len);
   const int pos_first = len - rb.tokens;   // position of the row's first query
 
@@ -328,10 +329,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
         }
       }
       const int4 miss = *reinterpret_cast<const int4 *>(s_miss[stage]);
-      const bool full = !__builtin_amdgcn_readfirstlane(miss.x | miss.y | miss.z | miss.w) &&
-                        t0 + PT <= all.hi && (t0 >= all.lo || t0 + PT <= a.sinks);
+      const int gone[4] = {__builtin_amdgcn_readfirstlane(miss.x), __builtin_amdgcn_readfirstlane(miss.y),
+                           __builtin_amdgcn_readfirstlane(miss.z), __builtin_amdgcn_readfirstlane(miss.w)};
+      const bool full = !(gone[0] | gone[1] | gone[2] | gone[3]) && t0 + PT <= all.hi &&
+                        (t0 >= all.lo || t0 + PT <= a.sinks);
       if (!full) {
-        const int gone[4] = {miss.x, miss.y, miss.z, miss.w};
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
