@@ -191,7 +191,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   const int64_t b1 = (b0 + 32 * WAVES < cols ? b0 + 32 * WAVES : cols) - 1;
   const int64_t c0 = b0 + wave * 32;                            // and of the wave
   const int64_t c1 = c0 + 31 < cols ? c0 + 31 : cols - 1;
-  const bool busy = c0 < cols;
   const int64_t cc = c0 + col;
   const bool there = cc < cols;
   const int64_t ccl = there ? cc : cols - 1;
@@ -200,10 +199,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   const auto lo_of = [&](int p) { return a.window <= p ? p + 1 - a.window : 0; };
   const Visible see = {lo_of(pos), pos + 1};
   const int wg0 = pos_first + (int)(b0 / a.group), wg1 = pos_first + (int)(b1 / a.group);
-  const int w0 = pos_first + (int)((busy ? c0 : b0) / a.group);
-  const int w1 = pos_first + (int)((busy ? c1 : b1) / a.group);
+  const int w0 = pos_first + (int)((c0 < cols ? c0 : b0) / a.group);
+  const int w1 = pos_first + (int)((c0 < cols ? c1 : b1) / a.group);
   const Visible any = {lo_of(wg0), wg1 + 1};                    // some column of the workgroup sees
-  const Visible some = {lo_of(w0), w1 + 1};                     // some column of the wave sees
   const Visible all = {lo_of(w1), w0 + 1};                      // every column of the wave sees
   const size_t qi = (size_t)(rb.begin + tok) * heads + (size_t)head * a.group + gq;
 
@@ -250,20 +248,33 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
     koff[j] = (uint32_t)((r - grp * 16) * ROWB + (c ^ key_swz<D>(r)) * 16);
     voff[j] = (uint32_t)((r - grp * 16) * ROWB + (c ^ value_swz<D>(r)) * 16);
   }
+  // Byte offset of the wave's group of tile i, or -1; asked for tile after tile.  A lane holds the
+  // page of one of the next 64 tiles, so that no tile waits for its table entry.
+  int ids = -1;
   const auto group_offset = [&](int i) -> int64_t {
-    return i < count ? group_at<ROWB>(pv, start_of(i) + grp * 16) : -1;
-  };
-  const auto issue = [&](int stage, int64_t at) {
-    if (at >= 0) {
-      const uint8_t *ks = tile::uniform_ptr(pv.k + at), *vs = tile::uniform_ptr(pv.v + at);
-      const uint32_t dst = lds0 + (uint32_t)stage * 2 * TILE + (uint32_t)row0 * ROWB;
-#pragma unroll
-      for (int j = 0; j < LOADS; ++j) {
-        tile::copy16_to_lds(ks, koff[j], dst + 1024u * j);
-        tile::copy16_to_lds(vs, voff[j], dst + TILE + 1024u * j);
-      }
+    if ((i & 63) == 0) {
+      const int pg = (start_of(i + lane) + grp * 16) >> pv.page_shift;
+      ids = i + lane < count && pg < pv.max_pages ? pv.table[pg] : -1;
     }
+    const int id = __builtin_amdgcn_readlane(ids, i & 63);
+    if (id < 0 || id >= pv.num_pages) return -1;
+    const int off = (start_of(i) + grp * 16) & ((1 << pv.page_shift) - 1);
+    return (int64_t)(((((size_t)id * pv.kv_heads + pv.head) << pv.page_shift) + off) * ROWB);
+  };
+  const auto copy_keys = [&](int stage, int64_t at) {
+    if (at < 0) return;
+    const uint8_t *src = tile::uniform_ptr(pv.k + at);
+    const uint32_t dst = lds0 + (uint32_t)stage * 2 * TILE + (uint32_t)row0 * ROWB;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) tile::copy16_to_lds(src, koff[j], dst + 1024u * j);
+  };
+  const auto copy_values = [&](int stage, int64_t at) {
     if (lane == 0) s_miss[stage][grp] = at < 0;
+    if (at < 0) return;
+    const uint8_t *src = tile::uniform_ptr(pv.v + at);
+    const uint32_t dst = lds0 + (uint32_t)stage * 2 * TILE + TILE + (uint32_t)row0 * ROWB;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) tile::copy16_to_lds(src, voff[j], dst + 1024u * j);
   };
   // after the copies have landed: values that no column sees become zeros (p = 0 does not undo
   // an infinity or NaN there)
@@ -301,97 +312,108 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   const int vr = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
   const int vel = (D / 2) * ((vr >> 2) & 1) + 4 * (vr >> 3);     // element of block 0
 
-  int64_t at = group_offset(0);
+  // the scores of the tile whose keys lie in `stage`
+  const auto scores = [&](int stage, float16_t (&s)[2]) {
+    const uint8_t *kt = s_kv[stage][0];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[kb][e] = 0.f;
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const uint4 ka = *reinterpret_cast<const uint4 *>(kt + kaddr[kb] + (((2 * c + h) ^ kswz) << 4));
+        mfma32<DT>(ka, q[c], s[kb]);
+      }
+    }
+  };
+
+  // Tile i's softmax and second product run while the scores of tile i + 1 are computed: keys are
+  // copied two tiles ahead, values one.
+  int64_t at_v = group_offset(0), at_k = group_offset(1);
+  float16_t s[2];
   if (count > 0) {
-    issue(0, at);
-    settle(0, 0, at);
+    copy_keys(0, at_v);
+    copy_values(0, at_v);
+    copy_keys(1, at_k);
+    settle(0, 0, at_v);
   }
-  int64_t at_next = group_offset(1);
   lds_barrier();
+  if (count > 0) scores(0, s);
   for (int i = 0; i < count; ++i) {
     const int stage = i & 1;
-    at = at_next;
-    if (i + 1 < count) issue(stage ^ 1, at);
-    at_next = group_offset(i + 2);
+    const int64_t at_now = at_k;             // tile i + 1
+    at_k = group_offset(i + 2);
     const int t0 = start_of(i);
-    const bool skip = !busy || t0 >= some.hi || (t0 + PT <= some.lo && t0 >= a.sinks);
-    if (!skip) {
-      const uint8_t *kt = s_kv[stage][0], *vt = s_kv[stage][1];
-      float16_t s[2];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[kb][e] = 0.f;
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          const uint4 ka = *reinterpret_cast<const uint4 *>(kt + kaddr[kb] + (((2 * c + h) ^ kswz) << 4));
-          mfma32<DT>(ka, q[c], s[kb]);
-        }
-      }
-      const int4 miss = *reinterpret_cast<const int4 *>(s_miss[stage]);
-      const int gone[4] = {__builtin_amdgcn_readfirstlane(miss.x), __builtin_amdgcn_readfirstlane(miss.y),
-                           __builtin_amdgcn_readfirstlane(miss.z), __builtin_amdgcn_readfirstlane(miss.w)};
-      const bool full = !(gone[0] | gone[1] | gone[2] | gone[3]) && t0 + PT <= all.hi &&
-                        (t0 >= all.lo || t0 + PT <= a.sinks);
-      if (!full) {
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int k = 32 * kb + 8 * (e >> 2) + (e & 3);   // + 4 h
-            if (gone[k >> 4] || !sees(see, a.sinks, t0 + k + 4 * h)) s[kb][e] = -__builtin_inff();
-          }
-      }
-      float top = s[0][0];
+    const int4 miss = *reinterpret_cast<const int4 *>(s_miss[stage]);
+    const int gone[4] = {__builtin_amdgcn_readfirstlane(miss.x), __builtin_amdgcn_readfirstlane(miss.y),
+                         __builtin_amdgcn_readfirstlane(miss.z), __builtin_amdgcn_readfirstlane(miss.w)};
+    if (i + 1 < count) copy_values(stage ^ 1, at_now);
+    if (i + 2 < count) copy_keys(stage, at_k);
+    const bool full = !(gone[0] | gone[1] | gone[2] | gone[3]) && t0 + PT <= all.hi &&
+                      (t0 >= all.lo || t0 + PT <= a.sinks);
+    if (!full) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kb][e]);
-      if (__any(top * scale2 > m + 8.f)) {
-        top = fmaxf(top, other_half(top)) * scale2;
-        const float grown = fmaxf(m, top);
-        const float nb = grown == -__builtin_inff() ? 0.f : grown;
-        const float keep = __builtin_amdgcn_exp2f(m - nb);
-        m = grown;
-        base = nb;
-        l *= keep;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[b][e] *= keep;
-      }
-      uint4 p[4];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        float x[16];
-#pragma unroll
         for (int e = 0; e < 16; ++e) {
-          x[e] = __builtin_amdgcn_exp2f(fmaf(s[kb][e], scale2, -base));
-          l += x[e];
+          const int k = 32 * kb + 8 * (e >> 2) + (e & 3);   // + 4 h
+          if (gone[k >> 4] || !sees(see, a.sinks, t0 + k + 4 * h)) s[kb][e] = -__builtin_inff();
         }
+    }
+    float top = s[0][0];
 #pragma unroll
-        for (int g2 = 0; g2 < 2; ++g2)
-          p[2 * kb + g2] = make_uint4(round2<DT>(x[8 * g2], x[8 * g2 + 1]), round2<DT>(x[8 * g2 + 2], x[8 * g2 + 3]),
-                                      round2<DT>(x[8 * g2 + 4], x[8 * g2 + 5]), round2<DT>(x[8 * g2 + 6], x[8 * g2 + 7]));
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kb][e]);
+    if (__any(top * scale2 > m + 8.f)) {
+      top = fmaxf(top, other_half(top)) * scale2;
+      const float grown = fmaxf(m, top);
+      const float nb = grown == -__builtin_inff() ? 0.f : grown;
+      const float keep = __builtin_amdgcn_exp2f(m - nb);
+      m = grown;
+      base = nb;
+      l *= keep;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[b][e] *= keep;
+    }
+    float16_t next[2];
+    scores(stage ^ 1, next);   // behind the last tile: of old keys, not used
+    const uint8_t *vt = s_kv[stage][1];
+    uint4 p[4];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = __builtin_amdgcn_exp2f(fmaf(s[kb][e], scale2, -base));
+        l += x[e];
       }
 #pragma unroll
-      for (int g2 = 0; g2 < 4; ++g2) {
+      for (int g2 = 0; g2 < 2; ++g2)
+        p[2 * kb + g2] = make_uint4(round2<DT>(x[8 * g2], x[8 * g2 + 1]), round2<DT>(x[8 * g2 + 2], x[8 * g2 + 3]),
+                                    round2<DT>(x[8 * g2 + 4], x[8 * g2 + 5]), round2<DT>(x[8 * g2 + 6], x[8 * g2 + 7]));
+    }
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          uint2 w[2];
+    for (int g2 = 0; g2 < 4; ++g2) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int r = 16 * g2 + 8 * u + vkey;
-            const int el = vel + 16 * b;
-            const uint8_t *src = vt + r * ROWB + (((el >> 3) ^ value_swz<D>(vkey)) << 4) + ((el & 7) << 1);
-            w[u] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)src));
-          }
-          mfma32<DT>(make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), p[g2], o[b]);
+      for (int b = 0; b < NB; ++b) {
+        uint2 w[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = 16 * g2 + 8 * u + vkey;
+          const int el = vel + 16 * b;
+          const uint8_t *src = vt + r * ROWB + (((el >> 3) ^ value_swz<D>(vkey)) << 4) + ((el & 7) << 1);
+          w[u] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)src));
         }
+        mfma32<DT>(make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), p[g2], o[b]);
       }
     }
-    if (i + 1 < count) settle(i + 1, stage ^ 1, at);
+    if (i + 1 < count) settle(i + 1, stage ^ 1, at_now);
     lds_barrier();
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) s[kb] = next[kb];
   }
   if (!there) return;
   l += other_half(l);
