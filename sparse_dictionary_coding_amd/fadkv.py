@@ -8,6 +8,7 @@ a missing library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -478,60 +479,91 @@ def fadkv_encode_omp(atoms: torch.Tensor, X: torch.Tensor, params: Params,
 
 
 # ---- the dense cache beside the codes ---------------------------------------------------------
+# A decode step calls these once per layer and their kernels take a few microseconds, so the
+# checks are written to cost little: one chain of comparisons per tensor, the messages apart.
 ROW_OK, ROW_REFUSED, ROW_RELEASED = 0, 1, 2    # FADKV_ROW_*
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BANDS, ROPE_YARN = 0, 1, 2, 3
 _ROPE = {"plain": ROPE_PLAIN, "linear": ROPE_LINEAR, "bands": ROPE_BANDS, "yarn": ROPE_YARN}
+_I32 = torch.int32
 
 
-def _inputs(device, **tensors):
-    """Every tensor given lies on `device`, and none of them expects a gradient: these calls have
-    no backward pass."""
-    grad = torch.is_grad_enabled()
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != device:
-            raise ValueError(f"{name} must live on {device}, got {t.device}")
-        if grad and t.requires_grad:
-            raise ValueError(f"{name} requires a gradient: this call has no backward pass "
-                             "(detach it or use torch.no_grad())")
+def _refuse(t, name: str, dtype, shape, dev: int):
+    """Raises what is wrong with the tensor, if anything is."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on cuda:{dev}, got {t.device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient: this call has no backward pass "
+                         "(detach it or use torch.no_grad())")
 
 
-class _Launch:
-    """The device a call runs on made current, and its stream: torch's current one of that device,
-    or the caller's, on which what the call allocates then lives."""
-
-    def __init__(self, device, stream):
-        self.device = device
-        self.stream = stream
-        self.stack = []
-
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.stack.append(torch.cuda.device(self.device))
-            self.stack[-1].__enter__()
-        if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
-        s = self.stream
-        if not hasattr(s, "cuda_stream"):
-            s = torch.cuda.ExternalStream(int(s), device=self.device)
-        self.stack.append(torch.cuda.stream(s))
-        self.stack[-1].__enter__()
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        while self.stack:
-            self.stack.pop().__exit__(*exc)
+def _ptr(t, name: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of this type and shape on this device, of which no gradient
+    is expected (the calls have no backward pass)."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or
+            t.get_device() != dev or t.requires_grad):
+        _refuse(t, name, dtype, shape, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-@dataclass
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must live on the GPU")
+    return dev
+
+
+@contextlib.contextmanager
+def _on(dev: int, stream):
+    """`dev` and the caller's stream (torch's current one of `dev` if none) made current: what a
+    call allocates then belongs to the stream that uses it."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        if stream.device.index != dev:
+            raise ValueError(f"the stream must be one of cuda:{dev}")
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _elsewhere(dev: int, stream) -> bool:
+    return stream is not None or dev != torch.cuda.current_device()
+
+
+def _raw_stream(dev: int) -> int:
+    """The handle of torch's current stream (torch.cuda.current_stream() builds an object first,
+    which takes as long as the rest of a call)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+@dataclass(frozen=True)
 class Pages:
     """One layer's dense cache: k and v [num_pages][kv_heads][page_size][d]."""
 
     k: torch.Tensor
     v: torch.Tensor
+
+    def __post_init__(self):
+        dev = _device_of(self.k, "pages.k")
+        if self.k.dim() != 4 or self.k.dtype not in _DT:
+            raise ValueError("pages must be [num_pages][kv_heads][page_size][d] "
+                             "float32/float16/bfloat16")
+        _ptr(self.k, "pages.k", self.k.dtype, self.k.shape, dev)
+        _ptr(self.v, "pages.v", self.k.dtype, self.k.shape, dev)
 
     @staticmethod
     def empty(num_pages: int, kv_heads: int, page_size: int, d: int, dtype, device) -> "Pages":
@@ -544,17 +576,11 @@ class Pages:
         return self.k.shape[2]
 
     def c(self) -> fadkv_pages:
-        k, v = self.k, self.v
-        if k.dim() != 4 or k.dtype not in _DT:
-            raise ValueError("pages must be [num_pages][kv_heads][page_size][d] "
-                             "float32/float16/bfloat16")
-        _check(k, "pages.k")
-        _check(v, "pages.v", k.dtype, k.shape)
-        n, h, p, d = k.shape
-        return fadkv_pages(n, p, h, d, _DT[k.dtype], k.data_ptr(), v.data_ptr())
+        n, h, p, d = self.k.shape
+        return fadkv_pages(n, p, h, d, _DT[self.k.dtype], self.k.data_ptr(), self.v.data_ptr())
 
 
-@dataclass
+@dataclass(frozen=True)
 class PageTable:
     """Which pages hold the rows of a batch, and which are free (fadkv_pages_advance)."""
 
@@ -564,16 +590,25 @@ class PageTable:
     ring_state: torch.Tensor   # int32 [2]: first free entry of ring, free entries
     page_size: int
 
+    def __post_init__(self):
+        dev = _device_of(self.table, "table")
+        if self.table.dim() != 2:
+            raise ValueError("table must be [R][max_pages]")
+        _ptr(self.table, "table", _I32, self.table.shape, dev)
+        _ptr(self.lens, "lens", _I32, self.table.shape[:1], dev)
+        _ptr(self.ring, "ring", _I32, (self.ring.numel(),), dev)
+        _ptr(self.ring_state, "ring_state", _I32, (2,), dev)
+
     @staticmethod
     def empty(rows: int, max_pages: int, num_pages: int, page_size: int, device) -> "PageTable":
         """No row holds a token; every page is free."""
-        return PageTable(torch.full((rows, max_pages), -1, dtype=torch.int32, device=device),
-                         torch.zeros(rows, dtype=torch.int32, device=device),
-                         torch.arange(num_pages, dtype=torch.int32, device=device),
-                         torch.tensor([0, num_pages], dtype=torch.int32, device=device), page_size)
+        return PageTable(torch.full((rows, max_pages), -1, dtype=_I32, device=device),
+                         torch.zeros(rows, dtype=_I32, device=device),
+                         torch.arange(num_pages, dtype=_I32, device=device),
+                         torch.tensor([0, num_pages], dtype=_I32, device=device), page_size)
 
 
-@dataclass
+@dataclass(frozen=True)
 class PageStep:
     """What fadkv_pages_advance writes.  lens and ring_state may be those of the PageTable."""
 
@@ -583,7 +618,18 @@ class PageStep:
     status: torch.Tensor       # int32 [R]: ROW_*
     slots: torch.Tensor        # int32 [max_tokens]
     positions: torch.Tensor    # int32 [max_tokens]
-    workspace: torch.Tensor
+    workspace: torch.Tensor    # uint8
+
+    def __post_init__(self):
+        dev = _device_of(self.lens, "lens")
+        R = self.lens.numel()
+        _ptr(self.lens, "lens", _I32, (R,), dev)
+        _ptr(self.ring_state, "ring_state", _I32, (2,), dev)
+        _ptr(self.cu, "cu", _I32, (R + 1,), dev)
+        _ptr(self.status, "status", _I32, (R,), dev)
+        _ptr(self.slots, "slots", _I32, (self.slots.numel(),), dev)
+        _ptr(self.positions, "positions", _I32, self.slots.shape, dev)
+        _ptr(self.workspace, "workspace", torch.uint8, self.workspace.shape, dev)
 
     @staticmethod
     def empty(pt: PageTable, max_tokens: int, in_place: bool = False) -> "PageStep":
@@ -596,7 +642,7 @@ class PageStep:
             raise FadkvError("fadkv_pages_workspace_bytes", st)
 
         def i32(n):
-            return torch.empty(n, dtype=torch.int32, device=dev)
+            return torch.empty(n, dtype=_I32, device=dev)
         return PageStep(pt.lens if in_place else i32(R), pt.ring_state if in_place else i32(2),
                         i32(R + 1), i32(R), i32(max_tokens), i32(max_tokens),
                         torch.empty(max(1, out.value), dtype=torch.uint8, device=dev))
@@ -606,39 +652,27 @@ def fadkv_pages_advance(pt: PageTable, new_lens: torch.Tensor, max_tokens: Optio
                         out: Optional[PageStep] = None, stream=None) -> PageStep:
     """One step of the bookkeeping: rows add new_lens [R] tokens (negative: the row has ended).
     pt.table and pt.ring are updated in place; give `out` (or the most tokens of a step)."""
-    dev = pt.table.device
-    i32 = torch.int32
-    _check(pt.table, "table", i32)
-    if pt.table.dim() != 2:
-        raise ValueError("table must be [R][max_pages]")
+    dev = pt.table.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return fadkv_pages_advance(pt, new_lens, max_tokens, out)
     R, max_pages = pt.table.shape
-    _check(pt.lens, "lens", i32, (R,))
-    _check(pt.ring, "ring", i32)
-    _check(pt.ring_state, "ring_state", i32, (2,))
-    _check(new_lens, "new_lens", i32, (R,))
-    if out is None and max_tokens is None:
-        raise ValueError("give out or max_tokens")
-    with _Launch(dev, stream) as strm:
-        if out is None:
-            out = PageStep.empty(pt, max_tokens)
-        if max_tokens is not None and max_tokens != out.slots.numel():
-            raise ValueError(f"out holds {out.slots.numel()} tokens, not {max_tokens}")
-        _check(out.lens, "out.lens", i32, (R,))
-        _check(out.ring_state, "out.ring_state", i32, (2,))
-        _check(out.cu, "out.cu", i32, (R + 1,))
-        _check(out.status, "out.status", i32, (R,))
-        _check(out.slots, "out.slots", i32)
-        _check(out.positions, "out.positions", i32, out.slots.shape)
-        _check(out.workspace, "out.workspace", torch.uint8)
-        _inputs(dev, lens=pt.lens, ring=pt.ring, ring_state=pt.ring_state, new_lens=new_lens,
-                out=out.cu, out_lens=out.lens, out_ring_state=out.ring_state, status=out.status,
-                slots=out.slots, positions=out.positions, workspace=out.workspace)
-        st = lib().fadkv_pages_advance(
-            pt.ring.numel(), pt.page_size, R, max_pages, new_lens.data_ptr(), pt.lens.data_ptr(),
-            pt.table.data_ptr(), pt.ring.data_ptr(), pt.ring_state.data_ptr(), out.slots.numel(),
-            out.lens.data_ptr(), out.ring_state.data_ptr(), out.cu.data_ptr(),
-            out.status.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
-            out.workspace.data_ptr(), out.workspace.numel(), strm)
+    new = _ptr(new_lens, "new_lens", _I32, (R,), dev)
+    if out is None:
+        if max_tokens is None:
+            raise ValueError("give out or max_tokens")
+        out = PageStep.empty(pt, max_tokens)
+    tokens = out.slots.shape[0]
+    if max_tokens is not None and max_tokens != tokens:
+        raise ValueError(f"out holds {tokens} tokens, not {max_tokens}")
+    if out.lens.shape[0] != R or out.lens.get_device() != dev:
+        raise ValueError(f"out must be for {R} rows on cuda:{dev}")
+    st = lib().fadkv_pages_advance(
+        pt.ring.shape[0], pt.page_size, R, max_pages, new, pt.lens.data_ptr(),
+        pt.table.data_ptr(), pt.ring.data_ptr(), pt.ring_state.data_ptr(), tokens,
+        out.lens.data_ptr(), out.ring_state.data_ptr(), out.cu.data_ptr(), out.status.data_ptr(),
+        out.slots.data_ptr(), out.positions.data_ptr(), out.workspace.data_ptr(),
+        out.workspace.numel(), _raw_stream(dev))
     if st != FADKV_OK:
         raise FadkvError("fadkv_pages_advance", st)
     return out
@@ -664,15 +698,11 @@ def fadkv_rope_freqs(rot_dim: int, base: float, kind: str = "plain", factor: flo
     return host.to(device), mscale.value
 
 
-def _heads(t: torch.Tensor, name: str, dtype, n: int, d: int) -> int:
-    """Checks [n][heads][d] whose heads lie together; returns the elements between tokens."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != d:
-        raise ValueError(f"{name} must be [{n}][heads][{d}], got {tuple(t.shape)}")
-    h = t.shape[1]
+def _heads(t: torch.Tensor, name: str, dtype, n: int, h: int, d: int, dev: int) -> int:
+    """Checks [n][h][d] whose heads lie together; returns the elements between tokens."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != (n, h, d) or
+            t.get_device() != dev or t.requires_grad):
+        _refuse(t, name, dtype, (n, h, d), dev)
     s0, s1, s2 = t.stride()
     if s2 != 1 or (h > 1 and s1 != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -689,52 +719,43 @@ def fadkv_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions
     """Norm (where a weight is given) and rotation of q [n][heads][d] and k [n][kv_heads][d],
     which may be views of one projection's output; keys and values also go to `slots` of `pages`
     and to k_rows, v_rows [kv_heads][n][d] (rows of the encoder).  Returns (or fills) q_out."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.dtype not in _DT:
+    dev = _device_of(q, "q")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return fadkv_norm_rope(q, k, v, positions, freqs, q_weight, k_weight, eps, interleaved,
+                                   mscale, pages, slots, q_out, k_rows, v_rows)
+    dt = q.dtype
+    if q.dim() != 3 or dt not in _DT:
         raise ValueError("q must be [n][heads][d] float32/float16/bfloat16")
-    if q.device.type != "cuda":
-        raise ValueError("q must live on the GPU")
-    dev, dt = q.device, q.dtype
     n, heads, d = q.shape
-    qs, ks, vs = _heads(q, "q", dt, n, d), _heads(k, "k", dt, n, d), _heads(v, "v", dt, n, d)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError(f"k must be [{n}][kv_heads][{d}]")
     kv = k.shape[1]
-    if v.shape[1] != kv:
-        raise ValueError(f"v must have {kv} heads as k, got {v.shape[1]}")
-    _check(positions, "positions", torch.int32, (n,))
-    rot = 0
+    qs = _heads(q, "q", dt, n, heads, d, dev)
+    ks = _heads(k, "k", dt, n, kv, d, dev)
+    vs = _heads(v, "v", dt, n, kv, d, dev)
+    pos = _ptr(positions, "positions", _I32, (n,), dev)
+    rot, fr = 0, None
     if freqs is not None:
-        _check(freqs, "freqs", torch.float64)
         rot = 2 * freqs.numel()
-    if q_weight is not None:
-        _check(q_weight, "q_weight", dt, (d,))
-    if k_weight is not None:
-        _check(k_weight, "k_weight", dt, (d,))
+        fr = _ptr(freqs, "freqs", torch.float64, (rot // 2,), dev) if rot else None
+    qw = None if q_weight is None else _ptr(q_weight, "q_weight", dt, (d,), dev)
+    kw = None if k_weight is None else _ptr(k_weight, "k_weight", dt, (d,), dev)
+    kr = None if k_rows is None else _ptr(k_rows, "k_rows", dt, (kv, n, d), dev)
+    vr = None if v_rows is None else _ptr(v_rows, "v_rows", dt, (kv, n, d), dev)
     if (pages is None) != (slots is None):
         raise ValueError("pages and slots go together")
-    if slots is not None:
-        _check(slots, "slots", torch.int32, (n,))
-    if k_rows is not None:
-        _check(k_rows, "k_rows", dt, (kv, n, d))
-    if v_rows is not None:
-        _check(v_rows, "v_rows", dt, (kv, n, d))
-    _inputs(dev, q=q, k=k, v=v, positions=positions, freqs=freqs, q_weight=q_weight,
-            k_weight=k_weight, slots=slots, k_rows=k_rows, v_rows=v_rows,
-            k_pages=pages and pages.k, v_pages=pages and pages.v, q_out=q_out)
-    with _Launch(dev, stream) as strm:
-        if q_out is None:
-            q_out = torch.empty(n, heads, d, dtype=dt, device=dev)
-        else:
-            _check(q_out, "q_out", dt, (n, heads, d))
-        a = fadkv_qkv(n, heads, kv, d, _DT[dt], q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks,
-                      vs, positions.data_ptr(),
-                      None if q_weight is None else q_weight.data_ptr(),
-                      None if k_weight is None else k_weight.data_ptr(), eps,
-                      freqs.data_ptr() if rot else None, rot, int(interleaved), mscale)
-        st = lib().fadkv_norm_rope(
-            ctypes.byref(a), q_out.data_ptr(),
-            None if pages is None else ctypes.byref(pages.c()),
-            None if slots is None else slots.data_ptr(),
-            None if k_rows is None else k_rows.data_ptr(),
-            None if v_rows is None else v_rows.data_ptr(), strm)
+    pg = sl = None
+    if pages is not None:
+        if pages.k.get_device() != dev:
+            raise ValueError(f"pages must live on cuda:{dev}")
+        pg, sl = ctypes.byref(pages.c()), _ptr(slots, "slots", _I32, (n,), dev)
+    if q_out is None:
+        q_out = torch.empty(n, heads, d, dtype=dt, device=q.device)
+    qo = _ptr(q_out, "q_out", dt, (n, heads, d), dev)
+    a = fadkv_qkv(n, heads, kv, d, _DT[dt], q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+                  pos, qw, kw, eps, fr, rot, interleaved, mscale)
+    st = lib().fadkv_norm_rope(ctypes.byref(a), qo, pg, sl, kr, vr, _raw_stream(dev))
     if st != FADKV_OK:
         raise FadkvError("fadkv_norm_rope", st)
     return q_out
@@ -749,17 +770,23 @@ def fadkv_attend_paged_workspace_bytes(pages: Pages, R: int, heads: int, max_len
     return int(out.value)
 
 
-def _attend_inputs(pages, table, lens, q, out):
-    _check(q, "q", pages.k.dtype)
-    if q.dim() != 3 or q.shape[2] != pages.k.shape[3]:
-        raise ValueError(f"q must be [..][heads][{pages.k.shape[3]}]")
-    _check(table, "table", torch.int32)
-    if table.dim() != 2:
-        raise ValueError("table must be [R][max_pages]")
-    _check(lens, "lens", torch.int32, (table.shape[0],))
-    if out is not None:
-        _check(out, "out", q.dtype, q.shape)
-    _inputs(q.device, q=q, table=table, lens=lens, k_pages=pages.k, v_pages=pages.v, out=out)
+def _attend_args(pages, table, lens, q, out, dev):
+    """Checks what both attention calls take; returns (pages struct, addresses, out, shapes)."""
+    p = pages.c()
+    dt = pages.k.dtype
+    if q.dim() != 3 or table.dim() != 2:
+        raise ValueError("q must be [..][heads][d] and table [R][max_pages]")
+    n, heads = q.shape[0], q.shape[1]
+    R, max_pages = table.shape
+    if pages.k.get_device() != dev:
+        raise ValueError(f"pages must live on cuda:{dev}")
+    qp = _ptr(q, "q", dt, (n, heads, p.d), dev)
+    tp = _ptr(table, "table", _I32, (R, max_pages), dev)
+    lp = _ptr(lens, "lens", _I32, (R,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    op = _ptr(out, "out", dt, (n, heads, p.d), dev)
+    return p, qp, tp, lp, op, out, n, heads, R, max_pages
 
 
 def fadkv_attend_paged(pages: Pages, table: torch.Tensor, lens: torch.Tensor, q: torch.Tensor,
@@ -769,27 +796,22 @@ def fadkv_attend_paged(pages: Pages, table: torch.Tensor, lens: torch.Tensor, q:
     """Attention of one new token per row, q [R][heads][d], over lens [R] cached tokens (its own
     included) in the pages of table [R][max_pages]; window > 0: only the last `window` tokens and
     the first `sinks` are visible.  Returns (or fills) out [R][heads][d]."""
-    p = pages.c()
-    _attend_inputs(pages, table, lens, q, out)
-    R, max_pages = table.shape
-    if q.shape[0] != R:
-        raise ValueError(f"q must have {R} rows, got {q.shape[0]}")
-    heads = q.shape[1]
+    dev = _device_of(q, "q")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return fadkv_attend_paged(pages, table, lens, q, scale, window, sinks, max_len, out,
+                                      workspace)
+    p, qp, tp, lp, op, out, n, heads, R, max_pages = _attend_args(pages, table, lens, q, out, dev)
+    if n != R:
+        raise ValueError(f"q must have {R} rows, got {n}")
     if max_len is None:
         max_len = max_pages * p.page_size
-    with _Launch(q.device, stream) as strm:
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
-            need = fadkv_attend_paged_workspace_bytes(pages, R, heads, max_len)
-            workspace = torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
-        else:
-            _check(workspace, "workspace", torch.uint8)
-            _inputs(q.device, workspace=workspace)
-        st = lib().fadkv_attend_paged(ctypes.byref(p), table.data_ptr(), max_pages,
-                                      lens.data_ptr(), R, q.data_ptr(), heads, scale, window,
-                                      sinks, max_len, out.data_ptr(), workspace.data_ptr(),
-                                      workspace.numel(), strm)
+    if workspace is None:
+        need = fadkv_attend_paged_workspace_bytes(pages, R, heads, max_len)
+        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
+    ws = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    st = lib().fadkv_attend_paged(ctypes.byref(p), tp, max_pages, lp, R, qp, heads, scale, window,
+                                  sinks, max_len, op, ws, workspace.numel(), _raw_stream(dev))
     if st != FADKV_OK:
         raise FadkvError("fadkv_attend_paged", st)
     return out
@@ -801,18 +823,14 @@ def fadkv_attend_prompt(pages: Pages, table: torch.Tensor, lens: torch.Tensor, c
     """Causal attention of packed tokens q [n][heads][d]: tokens cu[r] .. cu[r+1] - 1 are the last
     of row r's lens[r] cached ones.  Returns (or fills) out [n][heads][d]; rows of out behind the
     last token stay as they were (undefined where out is allocated here)."""
-    p = pages.c()
-    _attend_inputs(pages, table, lens, q, out)
-    R, max_pages = table.shape
-    _check(cu, "cu", torch.int32, (R + 1,))
-    _inputs(q.device, cu=cu)
-    n, heads = q.shape[0], q.shape[1]
-    with _Launch(q.device, stream) as strm:
-        if out is None:
-            out = torch.empty_like(q)
-        st = lib().fadkv_attend_prompt(ctypes.byref(p), table.data_ptr(), max_pages,
-                                       lens.data_ptr(), cu.data_ptr(), R, q.data_ptr(), n, heads,
-                                       scale, window, sinks, out.data_ptr(), strm)
+    dev = _device_of(q, "q")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return fadkv_attend_prompt(pages, table, lens, cu, q, scale, window, sinks, out)
+    p, qp, tp, lp, op, out, n, heads, R, max_pages = _attend_args(pages, table, lens, q, out, dev)
+    cp = _ptr(cu, "cu", _I32, (R + 1,), dev)
+    st = lib().fadkv_attend_prompt(ctypes.byref(p), tp, max_pages, lp, cp, R, qp, n, heads, scale,
+                                   window, sinks, op, _raw_stream(dev))
     if st != FADKV_OK:
         raise FadkvError("fadkv_attend_prompt", st)
     return out

@@ -614,10 +614,14 @@ def test_binding_refusals():
                     (ValueError, dict(lens=_i32([1, 2]))), (ValueError, dict(out=torch.empty(1, 3, 64, device=DEV).half())),
                     (ValueError, dict(q=torch.randn(1, 64, 2, device=DEV).half().transpose(1, 2))),
                     (ValueError, dict(q=q.clone().requires_grad_())),
-                    (fadkv.FadkvError, dict(window=-1)), (fadkv.FadkvError, dict(max_len=0)),
-                    (ValueError, dict(pages=fadkv.Pages(pages.k, pages.v[:, :, :, :32])))]:
+                    (fadkv.FadkvError, dict(window=-1)), (fadkv.FadkvError, dict(max_len=0))]:
         with pytest.raises(err):
             ok(**kw)
+    for err, kv in [(ValueError, (pages.k, pages.v[:, :, :, :32])), (TypeError, (pages.k, pages.v.float())),
+                    (ValueError, (pages.k.cpu(), pages.v)), (ValueError, (pages.k[0], pages.v[0])),
+                    (ValueError, (pages.k.transpose(0, 2), pages.v.transpose(0, 2)))]:
+        with pytest.raises(err):
+            fadkv.Pages(*kv)
     with torch.no_grad():
         ok(q=q.clone().requires_grad_())
     x = torch.randn(4, 6, 64, device=DEV).half()
@@ -634,6 +638,12 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         fadkv.fadkv_norm_rope(args[0], args[1], x[:, 4:5], *args[3:])
     pt = fadkv.PageTable.empty(2, 4, 8, 16, DEV)
+    with pytest.raises(ValueError):
+        fadkv.PageTable(pt.table, _i32([0]), pt.ring, pt.ring_state, 16)
+    with pytest.raises(TypeError):
+        fadkv.PageTable(pt.table, pt.lens, pt.ring.long(), pt.ring_state, 16)
+    with pytest.raises(ValueError):
+        fadkv.fadkv_pages_advance(pt, _i32([1, 1]), out=fadkv.PageStep.empty(fadkv.PageTable.empty(3, 4, 8, 16, DEV), 4))
     with pytest.raises(ValueError):
         fadkv.fadkv_pages_advance(pt, _i32([1, 1]))
     with pytest.raises(ValueError):
