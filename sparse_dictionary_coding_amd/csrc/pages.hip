@@ -25,8 +25,10 @@ constexpr int MAX_ROWS = 8192;                  // rows of one call: their cu fi
 constexpr int ONE_ROWS = SCAN_THREADS;          // one-workgroup form: a row per thread,
 constexpr int ONE_TOKENS = 4 * SCAN_THREADS;    // and a few tokens per thread
 
+// prefix sums over rows; need and back stay below R * max_pages < 2^31
 struct Sums {
-  long long add, need, back;
+  long long add;
+  uint32_t need, back;
 };
 
 __device__ __forceinline__ long long shfl_up_ll(long long v, int o) { return __shfl_up(v, o, 64); }
@@ -36,7 +38,8 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums &carry, Sums *s_wave) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const Sums u = {shfl_up_ll(v.add, o), shfl_up_ll(v.need, o), shfl_up_ll(v.back, o)};
+    const Sums u = {shfl_up_ll(v.add, o), (uint32_t)__shfl_up((int)v.need, o, 64),
+                    (uint32_t)__shfl_up((int)v.back, o, 64)};
     if (lane >= o) {
       v.add += u.add;
       v.need += u.need;
@@ -83,15 +86,16 @@ __device__ __forceinline__ void fill_token(const PagesArgs &a, int j, int r, boo
   a.positions[j] = pos;
 }
 
-// the row's new pages into its table, or its released ones into the ring (one wave)
-__device__ __forceinline__ void fill_pages(const PagesArgs &a, int r, const PageRow &row, int lane) {
+// pages i0, i0 + step, ... of the row's new ones into its table, or of its released ones into the ring
+__device__ __forceinline__ void fill_pages(const PagesArgs &a, int r, const PageRow &row, int i0,
+                                           int step) {
   int32_t *tab = a.table + (size_t)r * a.max_pages;
   if (row.pages > 0) {
     const int held = (int)(((int64_t)row.old + (1 << a.page_shift) - 1) >> a.page_shift);
-    for (int i = lane; i < row.pages; i += 64)
+    for (int i = i0; i < row.pages; i += step)
       tab[held + i] = a.ring[wrapped(row.first + i, a.num_pages)];
   } else {
-    for (int i = lane; i < -1 - row.pages; i += 64)
+    for (int i = i0; i < -1 - row.pages; i += step)
       a.ring[wrapped(row.first + i, a.num_pages)] = tab[i];
   }
 }
@@ -141,17 +145,18 @@ __global__ __launch_bounds__(SCAN_THREADS) void pages_scan_kernel(PagesArgs a) {
     const int need = !gone && fits ? (int)((len + add + P - 1) >> a.page_shift) - held : 0;
     // a table cannot name more pages than there are (lens of another table would say so)
     const int back = gone ? (held < a.num_pages ? held : a.num_pages) : 0;
-    const Sums s = block_scan({add, (long long)need, (long long)back}, carry, s_wave);
+    const Sums s = block_scan({add, (uint32_t)need, (uint32_t)back}, carry, s_wave);
     const bool ok = !gone && (add == 0 || (fits && s.add <= a.max_tokens &&
-                                           (need == 0 || s.need <= count)));
+                                           (need == 0 || s.need <= (uint32_t)count)));
     if (in) {
       PageRow row;
       row.old = len;
       row.pages = gone ? -1 - back : (ok ? need : 0);
-      // released pages go behind the free ones, new ones come from the head; both offsets are
-      // below 2^63 and only used where they are at most num_pages
-      row.first = gone ? (int)((head + (long long)count + s.back - back) % a.num_pages)
-                       : (ok ? (int)((head + s.need - need) % a.num_pages) : 0);
+      // released pages go behind the free ones, new ones come from the head (below 2^32 both; a row
+      // that is ok starts at most num_pages behind the head)
+      row.first = gone ? (int)(((uint32_t)head + (uint32_t)count + s.back - (uint32_t)back) %
+                               (uint32_t)a.num_pages)
+                       : (ok && need > 0 ? wrapped(head + (int)s.need - need, a.num_pages) : 0);
       row.ok = ok;
       if (ok && need > 0) atomicMax(&s_taken, (int)s.need);
       a.lens_out[r] = gone ? 0 : (ok ? (int)(len + add) : len);
@@ -169,7 +174,7 @@ __global__ __launch_bounds__(SCAN_THREADS) void pages_scan_kernel(PagesArgs a) {
   __syncthreads();
   if (tid == 0) {
     const int taken = s_taken;
-    a.ring_state_out[0] = (int)((head + (long long)taken) % a.num_pages);
+    a.ring_state_out[0] = wrapped(head + taken, a.num_pages);
     const long long left = (long long)count - taken + carry.back;
     a.ring_state_out[1] = (int)(left > a.num_pages ? a.num_pages : left);
   }
@@ -179,7 +184,19 @@ __global__ __launch_bounds__(SCAN_THREADS) void pages_scan_kernel(PagesArgs a) {
       const int r = in ? row_of(s_cu, a.R, j) : 0;
       fill_token(a, j, r, in, s_cu[r], s_row[r]);
     }
-    for (int r = tid >> 6; r < a.R; r += (int)(blockDim.x >> 6)) fill_pages(a, r, s_row[r], tid & 63);
+    // a thread moves its row's few pages, a wave those of each row with many
+    constexpr int FEW = 4;
+    int many = 0;
+    if (tid < a.R) {
+      const PageRow row = s_row[tid];
+      const int pages = row.pages >= 0 ? row.pages : -1 - row.pages;
+      many = pages > FEW;
+      if (!many) fill_pages(a, tid, row, 0, 1);
+    }
+    for (unsigned long long left = __ballot(many); left; left &= left - 1) {
+      const int r = (tid & ~63) + __builtin_ctzll(left);
+      fill_pages(a, r, s_row[r], tid & 63, 64);
+    }
   }
 }
 
@@ -189,7 +206,7 @@ __global__ __launch_bounds__(FILL_THREADS) void pages_fill_kernel(PagesArgs a, i
   const int tid = threadIdx.x;
   if ((int)blockIdx.x >= token_blocks) {
     const int r = ((int)blockIdx.x - token_blocks) * (FILL_THREADS / 64) + (tid >> 6);
-    if (r < a.R) fill_pages(a, r, a.rows[r], tid & 63);
+    if (r < a.R) fill_pages(a, r, a.rows[r], tid & 63, 64);
     return;
   }
   for (int r = tid; r <= a.R; r += FILL_THREADS) s_cu[r] = a.cu[r];
@@ -214,7 +231,8 @@ hipError_t launch_pages_advance(const PagesArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL(pages_scan_kernel<true>, dim3(1), dim3(threads), 0, stream, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(pages_scan_kernel<false>, dim3(1), dim3(SCAN_THREADS), 0, stream, a);
+  const int threads = a.R <= 64 ? 64 : (a.R <= 256 ? 256 : SCAN_THREADS);
+  hipLaunchKernelGGL(pages_scan_kernel<false>, dim3(1), dim3(threads), 0, stream, a);
   const int token_blocks = (int)(((int64_t)a.max_tokens + FILL_TOKENS - 1) / FILL_TOKENS);
   const int row_blocks = (a.R + FILL_THREADS / 64 - 1) / (FILL_THREADS / 64);
   if (token_blocks + row_blocks > 0)
