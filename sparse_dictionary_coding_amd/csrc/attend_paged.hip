@@ -5,9 +5,8 @@
 // one wave, for all query heads of its kv head (up to 16 columns of the matrix instruction), at
 // 4 d heads / (4 d kv_heads) = one to a few flops a byte.
 //
-// A row's 32-token tiles are split over `splits` workgroups (as many as fill the chip, counted
-// from the longest length; each takes an equal share of the row's own length) and dealt to a
-// workgroup's four waves in turn.  The waves' (maximum, sum, output) are joined in LDS, the
+// A row's 32-token tiles are split over up to `splits` workgroups, each an equal share of the row's
+// own length, and dealt to a workgroup's four waves in turn.  The waves' (maximum, sum, output) are joined in LDS, the
 // workgroups' through the workspace by a second kernel.
 #include "attend_tile.h"
 
@@ -16,14 +15,21 @@ namespace fadkv {
 namespace {
 
 constexpr int AP_WAVES = 4;
-constexpr int AP_TARGET = 1024;   // workgroups to aim for: four on each of the 256 CUs
-constexpr int AP_LEAST = 256;     // tokens below which a workgroup's share is not cut further
+constexpr int AP_FILL = 512;      // workgroups that are resident at once: two on each of the 256 CUs
+constexpr int AP_ROWS = 4;        // splits of a row of several
+constexpr int AP_LEAST = 256;     // tokens below which a share is not cut further
+constexpr int AP_JOIN = 4;        // waves that join a query's splits
 
 }  // namespace
 
+// As many splits as fill the chip in one round (measured at one row of 131072 tokens, 8 kv heads of
+// 128 in bf16: 512 workgroups 102 us, 1024 105, 2048 111), but four where there are several rows, so
+// that the end does not wait for the longest row (64 rows of 1 to 4096 tokens: four splits 115
+// us, one 120).
 int attend_paged_splits(int64_t R, int32_t kv_heads, int32_t group, int64_t visible) {
   const int64_t wgs = R * kv_heads * ((group + 15) / 16);
-  int64_t s = wgs > 0 ? (AP_TARGET + wgs - 1) / wgs : 1;
+  int64_t s = wgs > 0 ? (AP_FILL + wgs - 1) / wgs : 1;
+  if (R > 1 && s < AP_ROWS) s = AP_ROWS;
   const int64_t most = (visible + AP_LEAST - 1) / AP_LEAST;
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s);
@@ -50,12 +56,19 @@ __device__ __forceinline__ TileList tiles_of(int len, int window, int sinks) {
   return tl;
 }
 
+// tiles of a split: an equal share, no less than AP_LEAST tokens
+__device__ __forceinline__ int share_of(int count, int splits) {
+  const int share = (count + splits - 1) / splits;
+  return share < AP_LEAST / 32 ? AP_LEAST / 32 : share;
+}
+
 template <int DT, int D, bool SPLIT>
-__global__ __launch_bounds__(64 * AP_WAVES) void attend_paged_kernel(AttendArgs a) {
+__global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendArgs a) {
   using T = AttTile<DT, D>;
   __shared__ __attribute__((aligned(16))) float s_o[AP_WAVES][16][D + 4];
   __shared__ float s_m[AP_WAVES][16], s_l[AP_WAVES][16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // kv head fastest: workgroups of one kv head land on one chiplet (8 heads, 8 chiplets)
   const int blocks = (a.group + 15) >> 4;
   unsigned b = blockIdx.x;
@@ -71,8 +84,9 @@ __global__ __launch_bounds__(64 * AP_WAVES) void attend_paged_kernel(AttendArgs 
   int len = a.lens[r];
   len = len < 0 ? 0 : ((int64_t)len > room ? (int)room : len);
   const TileList tl = tiles_of(len, a.window, a.sinks);
-  const int share = SPLIT ? (tl.count + a.splits - 1) / a.splits : tl.count;
+  const int share = SPLIT ? share_of(tl.count, a.splits) : tl.count;
   const int i0 = SPLIT ? split * share : 0;
+  if (SPLIT && i0 >= tl.count) return;   // the join counts the splits that have tiles
   const int i1 = i0 + share < tl.count ? i0 + share : tl.count;
 
   const int col = lane & 15;
@@ -88,15 +102,47 @@ __global__ __launch_bounds__(64 * AP_WAVES) void attend_paged_kernel(AttendArgs 
   const Visible see = {a.window < len ? len - a.window : 0, len};
   const float scale2 = a.scale * kLog2e;
 
+  // Pages of the wave's tiles: lane k holds those of its k-th tile from here, so that a tile's
+  // loads wait for no table entry; and a tile is loaded while the one before it is worked on.
+  const auto start_of = [&](int i) { return (i < tl.first ? i : tl.from + i - tl.first) << 5; };
+  int ids0 = -1, ids1 = -1;
+  const auto fetch = [&](KvTile<DT, D> &kv, int i) {
+    const int k = (i - i0) / AP_WAVES;   // the wave's tile number
+    if ((k & 63) == 0) {
+      const int mine = i + lane * AP_WAVES;
+      ids0 = mine < i1 ? page_of(pv, start_of(mine)) : -1;
+      ids1 = mine < i1 ? page_of(pv, start_of(mine) + 16) : -1;
+    }
+    kv.load(pv, __builtin_amdgcn_readlane(ids0, k & 63), __builtin_amdgcn_readlane(ids1, k & 63),
+            start_of(i), lane);
+  };
   AttState<DT, D> st;
   st.clear();
-  for (int i = i0 + wave; i < i1; i += AP_WAVES) {
-    const int t0 = (i < tl.first ? i : tl.from + i - tl.first) << 5;
-    KvTile<DT, D> kv;
-    kv.load(pv, t0, lane);
+  const auto attend = [&](KvTile<DT, D> &kv, int i) {
+    const int t0 = start_of(i);
     const bool whole = kv.there[0] && kv.there[1] && t0 + 32 <= see.hi &&
                        (t0 >= see.lo || t0 + 32 <= a.sinks);
     attend_tile<DT, D>(kv, q, t0, whole, see, see, a.sinks, scale2, lane, st);
+  };
+  int i = i0 + wave;
+  if constexpr (DT == DT_F32) {   // two tiles of fp32 do not fit the registers of two waves a SIMD
+    KvTile<DT, D> kv;
+    for (; i < i1; i += AP_WAVES) {
+      fetch(kv, i);
+      attend(kv, i);
+    }
+  } else {
+    KvTile<DT, D> even, odd;
+    if (i < i1) fetch(even, i);
+    while (i < i1) {
+      if (i + AP_WAVES < i1) fetch(odd, i + AP_WAVES);
+      attend(even, i);
+      i += AP_WAVES;
+      if (i >= i1) break;
+      if (i + AP_WAVES < i1) fetch(even, i + AP_WAVES);
+      attend(odd, i);
+      i += AP_WAVES;
+    }
   }
 
   // join the waves
@@ -149,14 +195,22 @@ __global__ __launch_bounds__(64 * AP_WAVES) void attend_paged_kernel(AttendArgs 
 }
 
 // out[query] = the splits' outputs, each scaled from its own maximum to the common one, over the
-// sum; one wave per query, the splits in order
+// sum.  One workgroup per query: its waves take the splits in turn and are joined in LDS.
 template <int DT, int D>
-__global__ __launch_bounds__(64) void attend_join_kernel(AttendArgs a) {
+__global__ __launch_bounds__(64 * AP_JOIN) void attend_join_kernel(AttendArgs a) {
+  __shared__ float s_o[AP_JOIN][D], s_sum[AP_JOIN];
   const size_t qi = blockIdx.x;
-  const int lane = threadIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = (int)(qi / (unsigned)(a.kv_heads * a.group));
+  const int64_t room = (int64_t)a.max_pages << a.page_shift;
+  int len = a.lens[r];
+  len = len < 0 ? 0 : ((int64_t)len > room ? (int)room : len);
+  const int count = tiles_of(len, a.window, a.sinks).count;
+  const int share = share_of(count, a.splits);
+  const int used = (count + share - 1) / share;   // splits that had tiles
   const float2 *ml = a.part_ml + qi * a.splits;
   float m = -__builtin_inff();
-  for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, ml[s].x);
+  for (int s = lane; s < used; s += 64) m = fmaxf(m, ml[s].x);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   const float base = m == -__builtin_inff() ? 0.f : m;
@@ -166,21 +220,31 @@ __global__ __launch_bounds__(64) void attend_join_kernel(AttendArgs a) {
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   const float *po = a.part_o + qi * a.splits * D + lane * E;
 #pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
+  for (int s = wave; s < used; s += AP_JOIN) {
     const float2 x = ml[s];
     const float f = __builtin_amdgcn_exp2f(x.x - base);
     sum = fmaf(x.y, f, sum);
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = fmaf(po[(size_t)s * D + e], f, acc[e]);
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const size_t at = qi * D + lane * E + e;
-    const float y = acc[e] * inv;
-    if constexpr (DT == DT_F32) static_cast<float *>(a.out)[at] = y;
-    else static_cast<uint16_t *>(a.out)[at] = (uint16_t)round2<DT>(y, 0.f);
+  for (int e = 0; e < E; ++e) s_o[wave][lane * E + e] = acc[e];
+  if (lane == 0) s_sum[wave] = sum;
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  float y[2] = {0.f, 0.f};
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < AP_JOIN; ++w) {
+    sum += s_sum[w];
+    y[0] += s_o[w][2 * threadIdx.x];
+    y[1] += s_o[w][2 * threadIdx.x + 1];
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if constexpr (DT == DT_F32)
+    static_cast<float2 *>(a.out)[qi * (D / 2) + threadIdx.x] = make_float2(y[0] * inv, y[1] * inv);
+  else
+    static_cast<uint32_t *>(a.out)[qi * (D / 2) + threadIdx.x] = round2<DT>(y[0] * inv, y[1] * inv);
 }
 
 template <int DT, int D> static void attend_paged_run(const AttendArgs &a, hipStream_t stream) {
@@ -189,7 +253,7 @@ template <int DT, int D> static void attend_paged_run(const AttendArgs &a, hipSt
     hipLaunchKernelGGL((attend_paged_kernel<DT, D, true>), dim3(wgs * a.splits),
                        dim3(64 * AP_WAVES), 0, stream, a);
     hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3((unsigned)(a.R * a.kv_heads * a.group)),
-                       dim3(64), 0, stream, a);
+                       dim3(64 * AP_JOIN), 0, stream, a);
   } else {
     hipLaunchKernelGGL((attend_paged_kernel<DT, D, false>), dim3(wgs), dim3(64 * AP_WAVES), 0,
                        stream, a);

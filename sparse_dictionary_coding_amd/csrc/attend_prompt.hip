@@ -105,7 +105,8 @@ __global__ __launch_bounds__(64 * PR_WAVES) void attend_prompt_kernel(AttendArgs
       continue;
     }
     KvTile<DT, D> kv;
-    kv.load(pv, t0, lane);
+    kv.load(pv, __builtin_amdgcn_readfirstlane(page_of(pv, t0)),
+            __builtin_amdgcn_readfirstlane(page_of(pv, t0 + 16)), t0, lane);
     const bool whole = kv.there[0] && kv.there[1] && t0 + 32 <= all.hi &&
                        (t0 >= all.lo || t0 + 32 <= a.sinks);
     attend_tile<DT, D>(kv, q, t0, whole, see, any, a.sinks, scale2, lane, st);
@@ -252,14 +253,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   // page of one of the next 64 tiles, so that no tile waits for its table entry.
   int ids = -1;
   const auto group_offset = [&](int i) -> int64_t {
-    if ((i & 63) == 0) {
-      const int pg = (start_of(i + lane) + grp * 16) >> pv.page_shift;
-      ids = i + lane < count && pg < pv.max_pages ? pv.table[pg] : -1;
-    }
-    const int id = __builtin_amdgcn_readlane(ids, i & 63);
-    if (id < 0 || id >= pv.num_pages) return -1;
-    const int off = (start_of(i) + grp * 16) & ((1 << pv.page_shift) - 1);
-    return (int64_t)(((((size_t)id * pv.kv_heads + pv.head) << pv.page_shift) + off) * ROWB);
+    if ((i & 63) == 0) ids = i + lane < count ? page_of(pv, start_of(i + lane) + grp * 16) : -1;
+    return group_at<ROWB>(pv, __builtin_amdgcn_readlane(ids, i & 63), start_of(i) + grp * 16);
   };
   const auto copy_keys = [&](int stage, int64_t at) {
     if (at < 0) return;

@@ -39,12 +39,15 @@ struct PageView {
   int num_pages, page_shift, kv_heads, head, max_pages;
 };
 
-// byte offset of the 16 tokens from t0 (a multiple of 16; the same for all lanes), or -1 where no
-// valid page holds them
-template <int ROWB> __device__ __forceinline__ int64_t group_at(const PageView &pv, int t0) {
+// the page of the 16 tokens from t0 (a multiple of 16), -1 past the table
+__device__ __forceinline__ int page_of(const PageView &pv, int t0) {
   const int pg = t0 >> pv.page_shift;
-  if (t0 < 0 || pg >= pv.max_pages) return -1;
-  const int id = __builtin_amdgcn_readfirstlane(pv.table[pg]);
+  return pg < pv.max_pages ? pv.table[pg] : -1;
+}
+
+// byte offset of the 16 tokens from t0 in page id (scalars), or -1 where that is no page
+template <int ROWB>
+__device__ __forceinline__ int64_t group_at(const PageView &pv, int id, int t0) {
   if (id < 0 || id >= pv.num_pages) return -1;
   const int off = t0 & ((1 << pv.page_shift) - 1);
   return (int64_t)(((((size_t)id * pv.kv_heads + pv.head) << pv.page_shift) + off) * ROWB);
@@ -108,13 +111,14 @@ template <int DT, int D> struct KvTile {
   uint32_t v[8][AttTile<DT, D>::VW];
   bool there[2];
 
-  // Groups without a valid page read as zeros and are masked by the caller
-  __device__ __forceinline__ void load(const PageView &pv, int t0, int lane) {
+  // id0, id1: pages of the two 16-token groups (scalars).  Groups without a valid page read as
+  // zeros and are masked by the caller.
+  __device__ __forceinline__ void load(const PageView &pv, int id0, int id1, int t0, int lane) {
     using T = AttTile<DT, D>;
     const int r = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      const int64_t at = group_at<T::ROWB>(pv, t0 + 16 * a);
+      const int64_t at = group_at<T::ROWB>(pv, a ? id1 : id0, t0 + 16 * a);
       there[a] = at >= 0;
       if (there[a]) {
         const uint4 *src = reinterpret_cast<const uint4 *>(pv.k + at + (size_t)r * T::ROWB);
