@@ -10,9 +10,10 @@
 // partner elements of the half layout by a lane exchange of the packed input.
 //
 // Angles take 64 bits (at position 10^6 an fp32 product is already 0.06 rad off), which is far too
-// much per element; but a token's angles are the same for all its heads, so the workgroup first
-// computes cos and sin of its tokens' angles into LDS, one angle per thread, reduced to a part
-// of a turn in fp64 and evaluated in fp32.
+// much per element; but a token's angles are the same for all its heads, so a workgroup takes one
+// token and first computes cos and sin of its angles into LDS, one angle per thread, reduced to
+// a part of a turn in fp64 and evaluated in fp32 (two, four and eight tokens a workgroup measured
+// 3, 6 and 15 % slower at 16384 tokens).
 #include "common.h"
 #include "dense.h"
 
@@ -21,7 +22,11 @@ namespace fadkv {
 namespace {
 
 constexpr int NR_THREADS = 256;
-constexpr int NR_BATCH = 4;   // heads a lane group has in flight
+constexpr int NR_BATCH = 3;   // heads a lane group has in flight
+// Outputs beyond the eight L2s' 32 MB are stored around the caches: whatever reads them next would
+// not find the first of them there anyway, and the inputs that are still to come stay (16384
+// tokens, 302 MB written: 81 us against 106 us with plain stores).
+constexpr int64_t NR_STREAM = int64_t(32) << 20;
 
 // 8 elements of a row as they are stored
 template <int DT> struct Pack8 {
@@ -86,11 +91,17 @@ template <int DT> __device__ __forceinline__ Pack8<DT> load8(const uint8_t *row,
   return p;
 }
 
-template <int DT>
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+template <int DT, bool STREAM>
 __device__ __forceinline__ void store8(uint8_t *row, int lane, const Pack8<DT> &p) {
-  uint4 *dst = reinterpret_cast<uint4 *>(row) + lane * (DT == DT_F32 ? 2 : 1);
-  dst[0] = p.w[0];
-  if constexpr (DT == DT_F32) dst[1] = p.w[1];
+  u32x4_t *dst = reinterpret_cast<u32x4_t *>(row) + lane * (DT == DT_F32 ? 2 : 1);
+#pragma unroll
+  for (int i = 0; i < (DT == DT_F32 ? 2 : 1); ++i) {
+    const u32x4_t v = {p.w[i].x, p.w[i].y, p.w[i].z, p.w[i].w};
+    if constexpr (STREAM) __builtin_nontemporal_store(v, dst + i);
+    else dst[i] = v;
+  }
 }
 
 __device__ __forceinline__ uint4 shfl4(const uint4 &v, int from) {
@@ -100,33 +111,29 @@ __device__ __forceinline__ uint4 shfl4(const uint4 &v, int from) {
 
 }  // namespace
 
-// TOK tokens per workgroup, their heads (queries, keys, values in that order) dealt to lane groups
-template <int DT, int D, int TOK>
+// One token per workgroup, its heads (queries, keys, values in that order) dealt to lane groups
+template <int DT, int D, bool STREAM>
 __global__ __launch_bounds__(NR_THREADS) void norm_rope_kernel(NormRopeArgs a) {
   constexpr int W = D / 8;                  // lanes a head
   constexpr int GROUPS = NR_THREADS / W;
   constexpr int ES = Elem<DT>::bytes;
   constexpr int ROWB = D * ES;
-  __shared__ __attribute__((aligned(16))) float s_cos[TOK][D / 2], s_sin[TOK][D / 2];
-  __shared__ int s_pos[TOK], s_slot[TOK];
+  __shared__ __attribute__((aligned(16))) float s_cos[D / 2], s_sin[D / 2];
   const fadkv_qkv &in = a.in;
   const int tid = threadIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.x * TOK;
-  const int toks = (int)(in.n - t0 < TOK ? in.n - t0 : TOK);
+  const int64_t tok = blockIdx.x;
+  const int pos = in.positions[tok];
+  if (pos < 0) return;   // a padding token
+  const int slot = a.k_pages ? a.slots[tok] : -1;
   const int half = in.rot_dim >> 1;
-  if (tid < toks) {
-    s_pos[tid] = in.positions[t0 + tid];
-    s_slot[tid] = a.k_pages ? a.slots[t0 + tid] : -1;
-  }
-  for (int i = tid; i < toks * half; i += NR_THREADS) {
-    const int t = i / half, f = i - t * half;
+  if (tid < half) {
     // turns = position * f / 2 pi, reduced to [-1/2, 1/2]: 53 bits leave 2^-22 of a turn at 2^31
-    double turns = (double)in.positions[t0 + t] * (in.freqs[f] * 0.15915494309189533577);
+    double turns = (double)pos * (in.freqs[tid] * 0.15915494309189533577);
     turns -= __builtin_rint(turns);
     float sn, cs;
     sincospif((float)(turns + turns), &sn, &cs);
-    s_cos[t][f] = cs * in.mscale;
-    s_sin[t][f] = sn * in.mscale;
+    s_cos[tid] = cs * in.mscale;
+    s_sin[tid] = sn * in.mscale;
   }
   const int li = tid % W, grp = tid / W;
   const int lane = tid & 63;
@@ -147,17 +154,13 @@ __global__ __launch_bounds__(NR_THREADS) void norm_rope_kernel(NormRopeArgs a) {
   }
   __syncthreads();
 
-  const int per = in.heads + 2 * in.kv_heads;
-  const int items = toks * per;
-  for (int i0 = grp; i0 < items; i0 += GROUPS * NR_BATCH) {
+  const int heads = in.heads + 2 * in.kv_heads;
+  for (int h0 = grp; h0 < heads; h0 += GROUPS * NR_BATCH) {
     Pack8<DT> x[NR_BATCH];
 #pragma unroll
     for (int b = 0; b < NR_BATCH; ++b) {
-      const int it = i0 + b * GROUPS;
-      if (it < items) {
-        const int t = TOK == 1 ? 0 : it / per;
-        const int h = it - t * per;
-        const int64_t tok = t0 + t;
+      const int h = h0 + b * GROUPS;
+      if (h < heads) {
         const uint8_t *src;
         if (h < in.heads)
           src = static_cast<const uint8_t *>(in.q) + (size_t)(tok * in.q_stride) * ES + (size_t)h * ROWB;
@@ -172,12 +175,8 @@ __global__ __launch_bounds__(NR_THREADS) void norm_rope_kernel(NormRopeArgs a) {
     }
 #pragma unroll
     for (int b = 0; b < NR_BATCH; ++b) {
-      const int it = i0 + b * GROUPS;
-      if (it >= items) break;
-      const int t = TOK == 1 ? 0 : it / per;
-      const int h = it - t * per;
-      const int64_t tok = t0 + t;
-      if (s_pos[t] < 0) continue;
+      const int h = h0 + b * GROUPS;
+      if (h >= heads) break;
       const bool is_q = h < in.heads, is_v = h >= in.heads + in.kv_heads;
       Pack8<DT> out = x[b];
       if (!is_v) {
@@ -209,7 +208,7 @@ __global__ __launch_bounds__(NR_THREADS) void norm_rope_kernel(NormRopeArgs a) {
           if (in.interleaved) {
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-              const float c = s_cos[t][4 * li + e / 2], s = s_sin[t][4 * li + e / 2];
+              const float c = s_cos[4 * li + e / 2], s = s_sin[4 * li + e / 2];
               const float p = y[e], q = y[e + 1];
               y[e] = p * c - q * s;
               y[e + 1] = q * c + p * s;
@@ -218,7 +217,7 @@ __global__ __launch_bounds__(NR_THREADS) void norm_rope_kernel(NormRopeArgs a) {
             const int f = 8 * (second ? li - hl : li);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float c = s_cos[t][f + e], s = s_sin[t][f + e];
+              const float c = s_cos[f + e], s = s_sin[f + e];
               y[e] = y[e] * c + (second ? z[e] : -z[e]) * s;
             }
           }
@@ -226,31 +225,29 @@ __global__ __launch_bounds__(NR_THREADS) void norm_rope_kernel(NormRopeArgs a) {
         out = pack<DT>(y);
       }
       if (is_q) {
-        store8<DT>(static_cast<uint8_t *>(a.q_out) + (size_t)(tok * in.heads + h) * ROWB, li, out);
+        store8<DT, STREAM>(static_cast<uint8_t *>(a.q_out) + (size_t)(tok * in.heads + h) * ROWB, li, out);
       } else {
         const int kh = h - in.heads - (is_v ? in.kv_heads : 0);
-        const int slot = s_slot[t];
         if (slot >= 0 && slot < a.num_slots) {
           const int page = slot >> a.page_shift, off = slot & ((1 << a.page_shift) - 1);
           uint8_t *pages = static_cast<uint8_t *>(is_v ? a.v_pages : a.k_pages);
-          store8<DT>(pages + ((((size_t)page * in.kv_heads + kh) << a.page_shift) + off) * ROWB, li, out);
+          store8<DT, STREAM>(pages + ((((size_t)page * in.kv_heads + kh) << a.page_shift) + off) * ROWB, li, out);
         }
         uint8_t *rows = static_cast<uint8_t *>(is_v ? a.v_rows : a.k_rows);
-        if (rows) store8<DT>(rows + ((size_t)kh * in.n + tok) * ROWB, li, out);
+        if (rows) store8<DT, STREAM>(rows + ((size_t)kh * in.n + tok) * ROWB, li, out);
       }
     }
   }
 }
 
 template <int DT, int D> static void norm_rope_run(const NormRopeArgs &a, hipStream_t stream) {
-  // one token a workgroup until that fills the chip's 256 CUs four times over, then four (they
-  // share the weights' loads, and their angles fill the workgroup's threads)
-  if (a.in.n <= 1024)
-    hipLaunchKernelGGL((norm_rope_kernel<DT, D, 1>), dim3((unsigned)a.in.n), dim3(NR_THREADS), 0,
-                       stream, a);
+  const int64_t rows = a.in.heads + (int64_t)a.in.kv_heads *
+      ((a.k_pages ? 2 : 0) + (a.k_rows ? 1 : 0) + (a.v_rows ? 1 : 0));
+  const dim3 grid((unsigned)a.in.n);
+  if (a.in.n * rows * D * Elem<DT>::bytes > NR_STREAM)
+    hipLaunchKernelGGL((norm_rope_kernel<DT, D, true>), grid, dim3(NR_THREADS), 0, stream, a);
   else
-    hipLaunchKernelGGL((norm_rope_kernel<DT, D, 4>), dim3((unsigned)((a.in.n + 3) / 4)),
-                       dim3(NR_THREADS), 0, stream, a);
+    hipLaunchKernelGGL((norm_rope_kernel<DT, D, false>), grid, dim3(NR_THREADS), 0, stream, a);
 }
 
 hipError_t launch_norm_rope(const NormRopeArgs &a, hipStream_t stream) {
