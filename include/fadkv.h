@@ -386,11 +386,18 @@ int fadkv_attend_paged(const fadkv_pages *pages, const int32_t *table, int32_t m
  * position); a query whose position would be negative gives 0.
  *   cu device int32 [R+1], non-decreasing, cu[0] >= 0, taken as clamped to [0, n]
  *   q, out device [n][heads][d]; rows of out that belong to no token of a row stay as they were
- * n * heads <= 2^28; the other limits as above.  Needs no workspace. */
+ * n * heads <= 2^28; the other limits and max_len as above.  What a query does not see never
+ * reaches its output, infinities and NaN among other queries' tokens included (a block of queries
+ * that meets such a value is computed column by column, many times slower).
+ * workspace: fadkv_attend_prompt_workspace_bytes() bytes (0 where no split is needed: there are
+ * enough queries to fill the chip), 256-byte aligned. */
+int fadkv_attend_prompt_workspace_bytes(const fadkv_pages *pages, int64_t R, int64_t n,
+                                        int32_t heads, int32_t max_len, size_t *bytes);
 int fadkv_attend_prompt(const fadkv_pages *pages, const int32_t *table, int32_t max_pages,
                         const int32_t *lens, const int32_t *cu, int64_t R, const void *q,
                         int64_t n, int32_t heads, float scale, int32_t window, int32_t sinks,
-                        void *out, hipStream_t stream);
+                        int32_t max_len, void *out, void *workspace, size_t workspace_bytes,
+                        hipStream_t stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char *fadkv_status_string(int status);

@@ -91,11 +91,33 @@ fadkv::AttendArgs attend_args(const fadkv_pages *p, const int32_t *table, int32_
     if (_st != FADKV_OK) return _st; \
   } while (0)
 
-// [R][heads][splits] outputs of d floats, then as many (maximum, sum) pairs
-size_t attend_part_bytes(int64_t R, int32_t heads, int splits, int32_t d) {
+// [queries][splits] outputs of d floats, then as many (maximum, sum) pairs
+size_t attend_part_bytes(int64_t queries, int splits, int32_t d) {
   if (splits <= 1) return 0;
-  const size_t parts = (size_t)R * (size_t)heads * (size_t)splits;
+  const size_t parts = (size_t)queries * (size_t)splits;
   return (parts * ((size_t)d * sizeof(float) + 2 * sizeof(float)) + 255) / 256 * 256;
+}
+
+int take_parts(fadkv::AttendArgs &a, int64_t queries, int32_t d, void *workspace,
+               size_t workspace_bytes) {
+  const size_t need = attend_part_bytes(queries, a.splits, d);
+  if (need == 0) return FADKV_OK;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FADKV_ERR_WORKSPACE;
+  a.part_o = static_cast<float *>(workspace);
+  a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)queries * a.splits * d);
+  return FADKV_OK;
+}
+
+// tokens that one query can see, at most, rounded out to tiles at both ends
+int64_t visible_bound(int32_t max_len, int32_t window, int32_t sinks) {
+  const int64_t w = (int64_t)window + sinks + 128;
+  return window && w < max_len ? w : max_len;
+}
+
+int check_prompt(const fadkv_pages *p, int64_t R, int64_t n, int32_t heads) {
+  FADKV_TRY(check_heads(p, R, heads));
+  if (n < 0 || n > kMaxPromptHeads || n * heads > kMaxPromptHeads) return FADKV_ERR_SHAPE;
+  return FADKV_OK;
 }
 
 }  // namespace
@@ -231,7 +253,7 @@ int fadkv_attend_paged_workspace_bytes(const fadkv_pages *pages, int64_t R, int3
   FADKV_TRY(check_heads(pages, R, heads));
   if (max_len < 1) return FADKV_ERR_SHAPE;
   *bytes = attend_part_bytes(
-      R, heads, fadkv::attend_paged_splits(R, pages->kv_heads, heads / pages->kv_heads, max_len),
+      R * heads, fadkv::attend_paged_splits(R, pages->kv_heads, heads / pages->kv_heads, max_len),
       pages->d);
   return FADKV_OK;
 }
@@ -251,29 +273,36 @@ int fadkv_attend_paged(const fadkv_pages *pages, const int32_t *table, int32_t m
     return FADKV_ERR_ARG;
   fadkv::AttendArgs a =
       attend_args(pages, table, max_pages, lens, R, q, heads, scale, window, sinks, out);
-  // tokens a query can see, rounded out to tiles at both ends
-  int64_t visible = max_len;
-  if (window && (int64_t)window + sinks + 64 < visible) visible = (int64_t)window + sinks + 64;
-  a.splits = fadkv::attend_paged_splits(R, a.kv_heads, a.group, visible);
-  const size_t need = attend_part_bytes(R, heads, a.splits, pages->d);
-  if (need > 0) {
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
-      return FADKV_ERR_WORKSPACE;
-    a.part_o = static_cast<float *>(workspace);
-    a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)R * heads * a.splits * pages->d);
-  }
+  a.splits = fadkv::attend_paged_splits(R, a.kv_heads, a.group,
+                                        visible_bound(max_len, window, sinks));
+  FADKV_TRY(take_parts(a, R * heads, pages->d, workspace, workspace_bytes));
   return fadkv::launch_attend_paged(pages->dtype, pages->d, a, stream) == hipSuccess
              ? FADKV_OK : FADKV_ERR_HIP;
+}
+
+int fadkv_attend_prompt_workspace_bytes(const fadkv_pages *pages, int64_t R, int64_t n,
+                                        int32_t heads, int32_t max_len, size_t *bytes) {
+  if (!bytes) return FADKV_ERR_ARG;
+  FADKV_TRY(check_pages_shape(pages));
+  FADKV_TRY(check_prompt(pages, R, n, heads));
+  if (max_len < 1) return FADKV_ERR_SHAPE;
+  *bytes = attend_part_bytes(n * heads,
+                             fadkv::attend_prompt_splits(pages->dtype, R, n, pages->kv_heads,
+                                                         heads / pages->kv_heads, max_len),
+                             pages->d);
+  return FADKV_OK;
 }
 
 int fadkv_attend_prompt(const fadkv_pages *pages, const int32_t *table, int32_t max_pages,
                         const int32_t *lens, const int32_t *cu, int64_t R, const void *q,
                         int64_t n, int32_t heads, float scale, int32_t window, int32_t sinks,
-                        void *out, hipStream_t stream) {
+                        int32_t max_len, void *out, void *workspace, size_t workspace_bytes,
+                        hipStream_t stream) {
   FADKV_TRY(check_pages(pages));
-  FADKV_TRY(check_heads(pages, R, heads));
+  FADKV_TRY(check_prompt(pages, R, n, heads));
   FADKV_TRY(check_rows(pages, max_pages, scale, window, sinks));
-  if (n < 0 || n > kMaxPromptHeads || n * heads > kMaxPromptHeads) return FADKV_ERR_SHAPE;
+  if (max_len < 1 || (int64_t)max_len > (int64_t)max_pages * pages->page_size)
+    return FADKV_ERR_SHAPE;
   if (R == 0 || n == 0) return FADKV_OK;
   if (!table || !lens || !cu || !q || !out || !aligned(table, 4) || !aligned(lens, 4) ||
       !aligned(cu, 4) || !aligned(q, 16) || !aligned(out, 16))
@@ -282,6 +311,9 @@ int fadkv_attend_prompt(const fadkv_pages *pages, const int32_t *table, int32_t 
       attend_args(pages, table, max_pages, lens, R, q, heads, scale, window, sinks, out);
   a.cu = cu;
   a.n = n;
+  a.splits = fadkv::attend_prompt_splits(pages->dtype, R, n, a.kv_heads, a.group,
+                                         visible_bound(max_len, window, sinks));
+  FADKV_TRY(take_parts(a, n * heads, pages->d, workspace, workspace_bytes));
   return fadkv::launch_attend_prompt(pages->dtype, pages->d, a, stream) == hipSuccess
              ? FADKV_OK : FADKV_ERR_HIP;
 }

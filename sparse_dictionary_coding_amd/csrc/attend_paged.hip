@@ -86,12 +86,16 @@ __global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendAr
   const TileList tl = tiles_of(len, a.window, a.sinks);
   const int share = SPLIT ? share_of(tl.count, a.splits) : tl.count;
   const int i0 = SPLIT ? split * share : 0;
-  if (SPLIT && i0 >= tl.count) return;   // the join counts the splits that have tiles
   const int i1 = i0 + share < tl.count ? i0 + share : tl.count;
 
   const int col = lane & 15;
   const int gq = cb * 16 + col;
   const bool there = gq < a.group;
+  if (SPLIT && i0 >= tl.count) {   // a short row's later splits have nothing
+    const size_t qi = (size_t)r * heads + (size_t)head * a.group + gq;
+    if (tid < 16 && there) a.part_ml[qi * a.splits + split] = make_float2(-__builtin_inff(), 0.f);
+    return;
+  }
   const uint8_t *qrow = static_cast<const uint8_t *>(a.q) +
                         ((size_t)r * heads + (size_t)head * a.group + (there ? gq : 0)) * T::ROWB;
   uint4 q[T::CH];
@@ -122,7 +126,7 @@ __global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendAr
     const int t0 = start_of(i);
     const bool whole = kv.there[0] && kv.there[1] && t0 + 32 <= see.hi &&
                        (t0 >= see.lo || t0 + 32 <= a.sinks);
-    attend_tile<DT, D>(kv, q, t0, whole, see, see, a.sinks, scale2, lane, st);
+    attend_tile<DT, D, false>(kv, q, t0, whole, see, see, a.sinks, scale2, lane, st);
   };
   int i = i0 + wave;
   if constexpr (DT == DT_F32) {   // two tiles of fp32 do not fit the registers of two waves a SIMD
@@ -195,22 +199,20 @@ __global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendAr
 }
 
 // out[query] = the splits' outputs, each scaled from its own maximum to the common one, over the
-// sum.  One workgroup per query: its waves take the splits in turn and are joined in LDS.
+// sum; parts without a visible token (maximum -inf) are not read.  One workgroup per query: its
+// waves take the splits in turn and are joined in LDS.  With cu, queries of no row are left alone.
 template <int DT, int D>
 __global__ __launch_bounds__(64 * AP_JOIN) void attend_join_kernel(AttendArgs a) {
   __shared__ float s_o[AP_JOIN][D], s_sum[AP_JOIN];
   const size_t qi = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = (int)(qi / (unsigned)(a.kv_heads * a.group));
-  const int64_t room = (int64_t)a.max_pages << a.page_shift;
-  int len = a.lens[r];
-  len = len < 0 ? 0 : ((int64_t)len > room ? (int)room : len);
-  const int count = tiles_of(len, a.window, a.sinks).count;
-  const int share = share_of(count, a.splits);
-  const int used = (count + share - 1) / share;   // splits that had tiles
+  if (a.cu) {
+    const int64_t tok = (int64_t)(qi / (unsigned)(a.kv_heads * a.group));
+    if (tok < a.cu[0] || tok >= a.cu[a.R]) return;
+  }
   const float2 *ml = a.part_ml + qi * a.splits;
   float m = -__builtin_inff();
-  for (int s = lane; s < used; s += 64) m = fmaxf(m, ml[s].x);
+  for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, ml[s].x);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   const float base = m == -__builtin_inff() ? 0.f : m;
@@ -220,8 +222,9 @@ __global__ __launch_bounds__(64 * AP_JOIN) void attend_join_kernel(AttendArgs a)
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   const float *po = a.part_o + qi * a.splits * D + lane * E;
 #pragma unroll 4
-  for (int s = wave; s < used; s += AP_JOIN) {
+  for (int s = wave; s < a.splits; s += AP_JOIN) {
     const float2 x = ml[s];
+    if (x.x == -__builtin_inff() && x.y == 0.f) continue;
     const float f = __builtin_amdgcn_exp2f(x.x - base);
     sum = fmaf(x.y, f, sum);
 #pragma unroll
@@ -247,31 +250,40 @@ __global__ __launch_bounds__(64 * AP_JOIN) void attend_join_kernel(AttendArgs a)
     static_cast<uint32_t *>(a.out)[qi * (D / 2) + threadIdx.x] = round2<DT>(y[0] * inv, y[1] * inv);
 }
 
-template <int DT, int D> static void attend_paged_run(const AttendArgs &a, hipStream_t stream) {
+hipError_t launch_attend_join(int dtype, int d, const AttendArgs &a, int64_t queries,
+                              hipStream_t stream) {
+  const dim3 grid((unsigned)queries), block(64 * AP_JOIN);
+  if (dtype == DT_F32) {
+    if (d == 64) hipLaunchKernelGGL((attend_join_kernel<DT_F32, 64>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((attend_join_kernel<DT_F32, 128>), grid, block, 0, stream, a);
+  } else if (dtype == DT_F16) {
+    if (d == 64) hipLaunchKernelGGL((attend_join_kernel<DT_F16, 64>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((attend_join_kernel<DT_F16, 128>), grid, block, 0, stream, a);
+  } else {
+    if (d == 64) hipLaunchKernelGGL((attend_join_kernel<DT_BF16, 64>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((attend_join_kernel<DT_BF16, 128>), grid, block, 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+template <int DT, int D>
+static hipError_t attend_paged_run(const AttendArgs &a, hipStream_t stream) {
   const unsigned wgs = (unsigned)((size_t)a.R * a.kv_heads * ((a.group + 15) / 16));
   if (a.splits > 1) {
     hipLaunchKernelGGL((attend_paged_kernel<DT, D, true>), dim3(wgs * a.splits),
                        dim3(64 * AP_WAVES), 0, stream, a);
-    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3((unsigned)(a.R * a.kv_heads * a.group)),
-                       dim3(64 * AP_JOIN), 0, stream, a);
-  } else {
-    hipLaunchKernelGGL((attend_paged_kernel<DT, D, false>), dim3(wgs), dim3(64 * AP_WAVES), 0,
-                       stream, a);
+    return launch_attend_join(DT, D, a, (int64_t)a.R * a.kv_heads * a.group, stream);
   }
+  hipLaunchKernelGGL((attend_paged_kernel<DT, D, false>), dim3(wgs), dim3(64 * AP_WAVES), 0, stream, a);
+  return hipGetLastError();
 }
 
 hipError_t launch_attend_paged(int dtype, int d, const AttendArgs &a, hipStream_t stream) {
-  if (dtype == DT_F32) {
-    if (d == 64) attend_paged_run<DT_F32, 64>(a, stream);
-    else attend_paged_run<DT_F32, 128>(a, stream);
-  } else if (dtype == DT_F16) {
-    if (d == 64) attend_paged_run<DT_F16, 64>(a, stream);
-    else attend_paged_run<DT_F16, 128>(a, stream);
-  } else {
-    if (d == 64) attend_paged_run<DT_BF16, 64>(a, stream);
-    else attend_paged_run<DT_BF16, 128>(a, stream);
-  }
-  return hipGetLastError();
+  if (dtype == DT_F32)
+    return d == 64 ? attend_paged_run<DT_F32, 64>(a, stream) : attend_paged_run<DT_F32, 128>(a, stream);
+  if (dtype == DT_F16)
+    return d == 64 ? attend_paged_run<DT_F16, 64>(a, stream) : attend_paged_run<DT_F16, 128>(a, stream);
+  return d == 64 ? attend_paged_run<DT_BF16, 64>(a, stream) : attend_paged_run<DT_BF16, 128>(a, stream);
 }
 
 }  // namespace fadkv

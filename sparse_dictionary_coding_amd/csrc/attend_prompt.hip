@@ -20,7 +20,13 @@ namespace fadkv {
 
 namespace {
 
-constexpr int PR_WAVES = 4;
+constexpr int PR_WAVES = 4;     // fp32: 16 columns a wave
+constexpr int PM_WAVES = 4;     // 16 bits: 32 columns a wave
+// Few columns do not fill the chip: their tokens are then split over workgroups and joined, until
+// the two workgroups a CU holds are all there or a share falls to PR_LEAST (PM_LEAST) tokens.
+constexpr int PM_FILL = 512;
+constexpr int PR_LEAST = 64;
+constexpr int PM_LEAST = 256;
 
 // Workgroup -> (row, block of `per` columns): rows in order, ceil(tokens * group / per) blocks each.
 // Every lane of the wave gets the answer; row = R where the workgroup has none.
@@ -64,12 +70,48 @@ __device__ __forceinline__ RowBlock find_row(const AttendArgs &a, int64_t blk, i
 
 }  // namespace
 
-template <int DT, int D>
+// The visible tiles of columns that some tokens of [lo, hi) and the first `sinks` are visible to:
+// tiles [0, first) of the first tokens, then [from, from + count - first).
+struct Tiles {
+  int first, from, count;
+};
+
+__device__ __forceinline__ Tiles tiles_between(const Visible &any, int sinks, int tile) {
+  Tiles tl;
+  const int hi = any.hi > 0 ? any.hi : 0;
+  const int last = (hi + tile - 1) / tile;
+  tl.first = ((sinks < hi ? sinks : hi) + tile - 1) / tile;
+  tl.from = any.lo / tile;
+  if (tl.first >= tl.from) {   // they meet: one stretch
+    tl.from = tl.first > 0 ? 0 : tl.from;
+    tl.first = 0;
+  }
+  tl.count = tl.first + (last > tl.from ? last - tl.from : 0);
+  return tl;
+}
+
+// tiles [i0, i1) of a split: an equal share, `least` at least
+__device__ __forceinline__ void split_tiles(int count, int splits, int split, int least, int &i0,
+                                            int &i1) {
+  int share = (count + splits - 1) / splits;
+  share = share < least ? least : share;
+  const int64_t begin = (int64_t)split * share;
+  i0 = begin < count ? (int)begin : count;
+  i1 = i0 + share < count ? i0 + share : count;
+}
+
+// `blk` is kv head, then split, then block of columns, the first fastest
+template <int DT, int D, bool SPLIT>
 __global__ __launch_bounds__(64 * PR_WAVES) void attend_prompt_kernel(AttendArgs a) {
   using T = AttTile<DT, D>;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int head = (int)(blockIdx.x % a.kv_heads);
-  const RowBlock rb = find_row(a, blockIdx.x / a.kv_heads, 16 * PR_WAVES, lane);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  unsigned blk = blockIdx.x;
+  const int head = (int)(blk % a.kv_heads);
+  blk /= a.kv_heads;
+  const int split = SPLIT ? (int)(blk % a.splits) : 0;
+  if (SPLIT) blk /= a.splits;
+  const RowBlock rb = find_row(a, blk, 16 * PR_WAVES, lane);
   if (rb.row >= a.R) return;
   const int heads = a.kv_heads * a.group;
   const int64_t room = (int64_t)a.max_pages << a.page_shift;
@@ -97,28 +139,51 @@ __global__ __launch_bounds__(64 * PR_WAVES) void attend_prompt_kernel(AttendArgs
   const Visible all = {a.window <= pos1 ? pos1 + 1 - a.window : 0, pos0 + 1};
   const float scale2 = a.scale * kLog2e;
 
+  const Tiles tl = tiles_between(any, a.sinks, 32);
+  const auto start_of = [&](int i) { return (i < tl.first ? i : tl.from + i - tl.first) * 32; };
+  int i0 = 0, i1 = tl.count;
+  if constexpr (SPLIT) split_tiles(tl.count, a.splits, split, PR_LEAST / 32, i0, i1);
+
   AttState<DT, D> st;
   st.clear();
-  for (int t0 = 0; t0 < any.hi; t0 += 32) {
-    if (t0 >= a.sinks && t0 + 32 <= any.lo) {   // between the first tokens and the window
-      t0 = (any.lo & ~31) - 32;
-      continue;
-    }
+  bool fine = true;
+  for (int i = i0; i < i1 && fine; ++i) {
+    const int t0 = start_of(i);
     KvTile<DT, D> kv;
     kv.load(pv, __builtin_amdgcn_readfirstlane(page_of(pv, t0)),
             __builtin_amdgcn_readfirstlane(page_of(pv, t0 + 16)), t0, lane);
     const bool whole = kv.there[0] && kv.there[1] && t0 + 32 <= all.hi &&
                        (t0 >= all.lo || t0 + 32 <= a.sinks);
-    attend_tile<DT, D>(kv, q, t0, whole, see, any, a.sinks, scale2, lane, st);
+    fine = attend_tile<DT, D, true>(kv, q, t0, whole, see, any, a.sinks, scale2, lane, st);
+  }
+  if (!fine) {
+    for (int c = 0; c < 16 && c0 + c < cols; ++c) {
+      const Visible own = {__shfl(see.lo, c, 64), __shfl(see.hi, c, 64)};
+      const size_t cq = (size_t)__shfl((long long)qi, c, 64);
+      float o[D / 64], m, l;
+      attend_column<DT, D>(pv, static_cast<const uint8_t *>(a.q) + cq * T::ROWB, a.scale, own,
+                           a.sinks, start_of, i0, i1, 32, lane, o, m, l);
+      store_column<DT, D, SPLIT>(a, cq, split, lane, o, m, l);
+    }
+    return;
   }
   const float l = column_sum(st.l);
-  const float inv = l == 0.f ? 0.f : 1.f / l;   // no visible token: 0
   float x[D / 4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int e = 0; e < T::EP; ++e) x[T::EP * i + e] = st.o[e][i] * inv;
-  if (there) store_output<DT, D>(static_cast<uint8_t *>(a.out) + qi * T::ROWB, lane, x);
+    for (int e = 0; e < T::EP; ++e) x[T::EP * i + e] = st.o[e][i];
+  if (!there) return;
+  if constexpr (SPLIT) {
+    const size_t at = qi * a.splits + split;
+    store_output<DT_F32, D>(reinterpret_cast<uint8_t *>(a.part_o + at * D), lane, x);
+    if (lane < 16) a.part_ml[at] = make_float2(st.m, l);
+  } else {
+    const float inv = l == 0.f ? 0.f : 1.f / l;   // no visible token: 0
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) x[i] *= inv;
+    store_output<DT, D>(static_cast<uint8_t *>(a.out) + qi * T::ROWB, lane, x);
+  }
 }
 
 // ---- 16-bit types: LDS tiles of 64 tokens, v_mfma_f32_32x32x16 --------------------------------
@@ -160,7 +225,7 @@ __device__ __forceinline__ void lds_barrier() {
 
 }  // namespace
 
-template <int DT, int D, int WAVES>
+template <int DT, int D, int WAVES, bool SPLIT>
 __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(AttendArgs a) {
   constexpr int ROWB = 2 * D;
   constexpr int CPR = ROWB / 16;         // chunks per row
@@ -171,13 +236,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   constexpr int LOADS = ROWS_W * ROWB / 1024;
   static_assert(ROWS_W <= 16 && LOADS >= 1, "a wave copies rows of one 16-token group");
   __shared__ __attribute__((aligned(256))) uint8_t s_kv[2][2][TILE];   // [stage][K, V]
-  __shared__ int s_miss[2][4];           // [stage][16-token group]: no valid page
+  // [stage][16-token group]: 1, no valid page; 2, an infinity or NaN that only some columns see
+  __shared__ __attribute__((aligned(16))) int s_miss[2][4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, h = lane >> 5;
 
-  const int head = (int)(blockIdx.x % a.kv_heads);
-  RowBlock rb = find_row(a, blockIdx.x / a.kv_heads, 32 * WAVES, lane);
+  unsigned blk = blockIdx.x;
+  const int head = (int)(blk % a.kv_heads);
+  blk /= a.kv_heads;
+  const int split = SPLIT ? (int)(blk % a.splits) : 0;
+  if (SPLIT) blk /= a.splits;
+  RowBlock rb = find_row(a, blk, 32 * WAVES, lane);
   if (rb.row >= a.R) return;
   const int heads = a.kv_heads * a.group;
   const int64_t cols = (int64_t)rb.tokens * a.group;
@@ -203,6 +273,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   const int w0 = pos_first + (int)((c0 < cols ? c0 : b0) / a.group);
   const int w1 = pos_first + (int)((c0 < cols ? c1 : b1) / a.group);
   const Visible any = {lo_of(wg0), wg1 + 1};                    // some column of the workgroup sees
+  const Visible each = {lo_of(wg1), wg0 + 1};                   // every column of the workgroup sees
   const Visible all = {lo_of(w1), w0 + 1};                      // every column of the wave sees
   const size_t qi = (size_t)(rb.begin + tok) * heads + (size_t)head * a.group + gq;
 
@@ -226,16 +297,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
                  a.table + (size_t)rb.row * a.max_pages, a.num_pages, a.page_shift, a.kv_heads,
                  head, a.max_pages};
 
-  // the visible tiles of the workgroup: [0, first) of the first tokens, then [from, last)
-  const int last = any.hi > 0 ? (any.hi + PT - 1) / PT : 0;
-  int first = ((a.sinks < any.hi ? a.sinks : (any.hi > 0 ? any.hi : 0)) + PT - 1) / PT;
-  int from = any.lo / PT;
-  if (first >= from) {
-    from = first > 0 ? 0 : from;
-    first = 0;
-  }
-  const int count = first + (last > from ? last - from : 0);
-  const auto start_of = [&](int i) { return (i < first ? i : from + i - first) * PT; };
+  const Tiles tl = tiles_between(any, a.sinks, PT);
+  const auto start_of = [&](int i) { return (i < tl.first ? i : tl.from + i - tl.first) * PT; };
+  int i0 = 0, count = tl.count;   // tiles [i0, count)
+  if constexpr (SPLIT) split_tiles(tl.count, a.splits, split, PM_LEAST / PT, i0, count);
 
   // this wave's rows of a tile: ROWS_W of the 16-token group grp
   const int grp = wave * ROWS_W / 16;
@@ -253,8 +318,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   // page of one of the next 64 tiles, so that no tile waits for its table entry.
   int ids = -1;
   const auto group_offset = [&](int i) -> int64_t {
-    if ((i & 63) == 0) ids = i + lane < count ? page_of(pv, start_of(i + lane) + grp * 16) : -1;
-    return group_at<ROWB>(pv, __builtin_amdgcn_readlane(ids, i & 63), start_of(i) + grp * 16);
+    if (((i - i0) & 63) == 0) ids = i + lane < count ? page_of(pv, start_of(i + lane) + grp * 16) : -1;
+    return group_at<ROWB>(pv, __builtin_amdgcn_readlane(ids, (i - i0) & 63), start_of(i) + grp * 16);
   };
   const auto copy_keys = [&](int stage, int64_t at) {
     if (at < 0) return;
@@ -271,19 +336,30 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) tile::copy16_to_lds(src, voff[j], dst + 1024u * j);
   };
-  // after the copies have landed: values that no column sees become zeros (p = 0 does not undo
-  // an infinity or NaN there)
+  // After the copies have landed, where not every column sees the whole tile: values that no column
+  // sees become zeros, as p = 0 does not undo an infinity or NaN; one that only some columns see
+  // cannot be kept from the others here and sends the block to attend_column.
   const auto settle = [&](int i, int stage, int64_t at) {
     tile::wait_vmem();
     asm volatile("" ::: "memory");
     const int t0 = start_of(i);
-    if (at < 0 || t0 + PT > any.hi || (t0 < any.lo && t0 + PT > a.sinks)) {
+    if (at < 0 || t0 + PT > each.hi || (t0 < each.lo && t0 + PT > a.sinks)) {
       constexpr int LPR = 64 / ROWS_W;   // lanes per row
       const int r = row0 + lane / LPR;
-      if (at < 0 || !sees(any, a.sinks, t0 + r)) {
-        uint4 *dst = reinterpret_cast<uint4 *>(&s_kv[stage][1][r * ROWB]);
-        for (int c = lane % LPR; c < CPR; c += LPR) dst[c] = make_uint4(0, 0, 0, 0);
+      const bool seen = at >= 0 && sees(any, a.sinks, t0 + r);
+      uint4 *row = reinterpret_cast<uint4 *>(&s_kv[stage][1][r * ROWB]);
+      bool bad = false;
+#pragma unroll
+      for (int c = 0; c < CPR; c += LPR) {
+        uint4 *at16 = row + c + lane % LPR;
+        if (seen) {
+          const uint4 w = *at16;
+          bad |= odd_value<DT>(w.x) || odd_value<DT>(w.y) || odd_value<DT>(w.z) || odd_value<DT>(w.w);
+        } else {
+          *at16 = make_uint4(0, 0, 0, 0);
+        }
       }
+      if (__any(bad) && lane == 0) s_miss[stage][grp] = 2;
     }
     tile::wait_lds();
   };
@@ -324,24 +400,30 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
 
   // Tile i's softmax and second product run while the scores of tile i + 1 are computed: keys are
   // copied two tiles ahead, values one.
-  int64_t at_v = group_offset(0), at_k = group_offset(1);
+  const int64_t at_v = group_offset(i0);
+  int64_t at_k = group_offset(i0 + 1);
   float16_t s[2];
-  if (count > 0) {
+  bool fine = true;
+  if (i0 < count) {
     copy_keys(0, at_v);
     copy_values(0, at_v);
     copy_keys(1, at_k);
-    settle(0, 0, at_v);
+    settle(i0, 0, at_v);
   }
   lds_barrier();
-  if (count > 0) scores(0, s);
-  for (int i = 0; i < count; ++i) {
-    const int stage = i & 1;
-    const int64_t at_now = at_k;             // tile i + 1
-    at_k = group_offset(i + 2);
-    const int t0 = start_of(i);
+  if (i0 < count) scores(0, s);
+  for (int i = i0; i < count; ++i) {
+    const int stage = (i - i0) & 1;
     const int4 miss = *reinterpret_cast<const int4 *>(s_miss[stage]);
     const int gone[4] = {__builtin_amdgcn_readfirstlane(miss.x), __builtin_amdgcn_readfirstlane(miss.y),
                          __builtin_amdgcn_readfirstlane(miss.z), __builtin_amdgcn_readfirstlane(miss.w)};
+    if ((gone[0] | gone[1] | gone[2] | gone[3]) & 2) {   // the same for all waves
+      fine = false;
+      break;
+    }
+    const int64_t at_now = at_k;             // tile i + 1
+    at_k = group_offset(i + 2);
+    const int t0 = start_of(i);
     if (i + 1 < count) copy_values(stage ^ 1, at_now);
     if (i + 2 < count) copy_keys(stage, at_k);
     const bool full = !(gone[0] | gone[1] | gone[2] | gone[3]) && t0 + PT <= all.hi &&
@@ -410,8 +492,30 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) s[kb] = next[kb];
   }
+  if (!fine) {
+    for (int c = 0; c < 32 && c0 + c < cols; ++c) {
+      const Visible own = {__shfl(see.lo, c, 64), __shfl(see.hi, c, 64)};
+      const size_t cq = (size_t)__shfl((long long)qi, c, 64);
+      float co[D / 64], cm, cl;
+      attend_column<DT, D>(pv, static_cast<const uint8_t *>(a.q) + cq * ROWB, a.scale, own, a.sinks,
+                           start_of, i0, count, PT, lane, co, cm, cl);
+      store_column<DT, D, SPLIT>(a, cq, split, lane, co, cm, cl);
+    }
+    return;
+  }
   if (!there) return;
   l += other_half(l);
+  if constexpr (SPLIT) {
+    const size_t at = qi * a.splits + split;
+    float4 *dst = reinterpret_cast<float4 *>(a.part_o + at * D + h * (D / 2));
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        dst[4 * b + u] = make_float4(o[b][4 * u], o[b][4 * u + 1], o[b][4 * u + 2], o[b][4 * u + 3]);
+    if (h == 0) a.part_ml[at] = make_float2(m, l);
+    return;
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;   // no visible token: 0
   uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + qi * ROWB + h * D);
 #pragma unroll
@@ -426,33 +530,47 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
     }
 }
 
-constexpr int PM_WAVES = 4;
-
-template <int DT, int D> static void attend_prompt_mfma_run(const AttendArgs &a, hipStream_t stream) {
-  const int64_t blocks = a.n * a.group / (32 * PM_WAVES) + (a.R < a.n ? a.R : a.n);
-  hipLaunchKernelGGL((attend_prompt_mfma_kernel<DT, D, PM_WAVES>),
-                     dim3((unsigned)(blocks * a.kv_heads)), dim3(64 * PM_WAVES), 0, stream, a);
+// Columns per workgroup; at most one started block more per row than the columns fill.
+static int64_t prompt_blocks(int dtype, int64_t R, int64_t n, int32_t group) {
+  const int per = dtype == DT_F32 ? 16 * PR_WAVES : 32 * PM_WAVES;
+  return n * group / per + (R < n ? R : n);
 }
 
-template <int DT, int D> static void attend_prompt_run(const AttendArgs &a, hipStream_t stream) {
-  // at most one started block more per row than the columns fill
-  const int64_t blocks = a.n * a.group / (16 * PR_WAVES) + (a.R < a.n ? a.R : a.n);
-  hipLaunchKernelGGL((attend_prompt_kernel<DT, D>), dim3((unsigned)(blocks * a.kv_heads)),
-                     dim3(64 * PR_WAVES), 0, stream, a);
+int attend_prompt_splits(int dtype, int64_t R, int64_t n, int32_t kv_heads, int32_t group,
+                         int64_t visible) {
+  const int64_t wgs = prompt_blocks(dtype, R, n, group) * kv_heads;
+  int64_t s = wgs > 0 ? (PM_FILL + wgs - 1) / wgs : 1;
+  const int64_t least = dtype == DT_F32 ? PR_LEAST : PM_LEAST;
+  const int64_t most = (visible + least - 1) / least;
+  s = s < most ? s : most;
+  return (int)(s < 1 ? 1 : s);
+}
+
+template <int DT, int D>
+static hipError_t attend_prompt_run(const AttendArgs &a, hipStream_t stream) {
+  const int64_t wgs = prompt_blocks(DT, a.R, a.n, a.group) * a.kv_heads;
+  const dim3 grid((unsigned)(wgs * a.splits));
+  if constexpr (DT == DT_F32) {
+    const dim3 block(64 * PR_WAVES);
+    if (a.splits > 1) hipLaunchKernelGGL((attend_prompt_kernel<DT, D, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((attend_prompt_kernel<DT, D, false>), grid, block, 0, stream, a);
+  } else {
+    const dim3 block(64 * PM_WAVES);
+    if (a.splits > 1)
+      hipLaunchKernelGGL((attend_prompt_mfma_kernel<DT, D, PM_WAVES, true>), grid, block, 0, stream, a);
+    else
+      hipLaunchKernelGGL((attend_prompt_mfma_kernel<DT, D, PM_WAVES, false>), grid, block, 0, stream, a);
+  }
+  if (a.splits > 1) return launch_attend_join(DT, D, a, a.n * a.kv_heads * a.group, stream);
+  return hipGetLastError();
 }
 
 hipError_t launch_attend_prompt(int dtype, int d, const AttendArgs &a, hipStream_t stream) {
-  if (dtype == DT_F32) {
-    if (d == 64) attend_prompt_run<DT_F32, 64>(a, stream);
-    else attend_prompt_run<DT_F32, 128>(a, stream);
-  } else if (dtype == DT_F16) {
-    if (d == 64) attend_prompt_mfma_run<DT_F16, 64>(a, stream);
-    else attend_prompt_mfma_run<DT_F16, 128>(a, stream);
-  } else {
-    if (d == 64) attend_prompt_mfma_run<DT_BF16, 64>(a, stream);
-    else attend_prompt_mfma_run<DT_BF16, 128>(a, stream);
-  }
-  return hipGetLastError();
+  if (dtype == DT_F32)
+    return d == 64 ? attend_prompt_run<DT_F32, 64>(a, stream) : attend_prompt_run<DT_F32, 128>(a, stream);
+  if (dtype == DT_F16)
+    return d == 64 ? attend_prompt_run<DT_F16, 64>(a, stream) : attend_prompt_run<DT_F16, 128>(a, stream);
+  return d == 64 ? attend_prompt_run<DT_BF16, 64>(a, stream) : attend_prompt_run<DT_BF16, 128>(a, stream);
 }
 
 }  // namespace fadkv

@@ -152,10 +152,19 @@ template <int DT, int D> struct KvTile {
   }
 };
 
+// an infinity or NaN among the values of a 32-bit word (two in the 16-bit types)
+template <int DT> __device__ __forceinline__ bool odd_value(uint32_t w) {
+  constexpr uint32_t E = DT == DT_F32 ? 0x7f800000u : (DT == DT_F16 ? 0x7c00u : 0x7f80u);
+  if constexpr (DT == DT_F32) return (w & E) == E;
+  else return (w & E) == E || ((w >> 16) & E) == E;
+}
+
 // One tile against the wave's 16 columns.  `whole`: every column sees all 32 tokens (uniform).
-// Tokens that no column sees are zeroed in v: p = 0 does not undo an infinity or NaN there.
-template <int DT, int D>
-__device__ __forceinline__ void attend_tile(KvTile<DT, D> &kv, const uint4 (&q)[AttTile<DT, D>::CH],
+// Tokens that no column sees are zeroed in v: p = 0 does not undo an infinity or NaN there.  Where
+// the columns see different tokens (MIXED) the same holds for a token that some of them see: then
+// nothing is done and the answer is false (attend_column does such blocks).
+template <int DT, int D, bool MIXED>
+__device__ __forceinline__ bool attend_tile(KvTile<DT, D> &kv, const uint4 (&q)[AttTile<DT, D>::CH],
                                             int t0, bool whole, const Visible &col,
                                             const Visible &any, int sinks, float scale2, int lane,
                                             AttState<DT, D> &st) {
@@ -180,6 +189,14 @@ __device__ __forceinline__ void attend_tile(KvTile<DT, D> &kv, const uint4 (&q)[
 #pragma unroll
         for (int c = 0; c < T::VW; ++c) kv.v[j][c] = 0;
       }
+    }
+    if constexpr (MIXED) {
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int c = 0; c < T::VW; ++c) bad |= odd_value<DT>(kv.v[j][c]);
+      if (__any(bad)) return false;
     }
   }
   float top = z[0];
@@ -223,6 +240,78 @@ __device__ __forceinline__ void attend_tile(KvTile<DT, D> &kv, const uint4 (&q)[
       mfma16<DT>(va, pb, st.o[e]);
     }
   }
+  return true;
+}
+
+// One column by itself over tiles [i0, i1) of `step` <= 64 tokens, a token per lane: nothing that the
+// column does not see is multiplied, whatever it holds.  The path of blocks that
+// hold an infinity or NaN where the tiles above cannot keep it from the columns that do not see it.
+// Lane l ends up with elements l D / 64 .. of the output, not yet divided by the sum; (m, l) likewise.
+template <int DT, int D, class Start>
+__device__ __forceinline__ void attend_column(const PageView &pv, const uint8_t *qrow, float scale,
+                                              const Visible &see, int sinks, Start start_of, int i0,
+                                              int i1, int step, int lane, float (&o)[D / 64],
+                                              float &m, float &l) {
+  constexpr int E = D / 64, ROWB = D * Elem<DT>::bytes;
+  const float scale2 = scale * kLog2e;
+  m = -__builtin_inff();
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int i = i0; i < i1; ++i) {
+    const int t = start_of(i) + lane;
+    bool on = lane < step && sees(see, sinks, t);
+    const int id = on ? page_of(pv, t) : -1;
+    on = id >= 0 && id < pv.num_pages;
+    const int off = t & ((1 << pv.page_shift) - 1);
+    const int64_t at =
+        on ? (int64_t)(((((size_t)id * pv.kv_heads + pv.head) << pv.page_shift) + off) * ROWB) : 0;
+    float z = -__builtin_inff();
+    if (on) {
+      float dot = 0.f;
+      for (int e = 0; e < D; ++e) dot = fmaf(elem_f<DT>(qrow, e), elem_f<DT>(pv.k + at, e), dot);
+      z = dot * scale2;
+    }
+    float top = z;
+#pragma unroll
+    for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
+    const float grown = fmaxf(m, top);
+    const float base = grown == -__builtin_inff() ? 0.f : grown;
+    const float keep = __builtin_amdgcn_exp2f(m - base);
+    m = grown;
+    const float p = on ? __builtin_amdgcn_exp2f(z - base) : 0.f;
+    l = fmaf(l, keep, wave_sum(p));
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= keep;
+    for (unsigned long long left = __ballot(on); left; left &= left - 1) {
+      const int j = __builtin_ctzll(left);
+      const float pj = __shfl(p, j, 64);
+      const uint8_t *row = pv.v + __shfl((long long)at, j, 64);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(pj, elem_f<DT>(row, lane * E + e), o[e]);
+    }
+  }
+}
+
+// and stores it: a part of a split, or the output
+template <int DT, int D, bool SPLIT>
+__device__ __forceinline__ void store_column(const AttendArgs &a, size_t qi, int split, int lane,
+                                             const float (&o)[D / 64], float m, float l) {
+  constexpr int E = D / 64;
+  if constexpr (SPLIT) {
+    const size_t at = qi * a.splits + split;
+#pragma unroll
+    for (int e = 0; e < E; ++e) a.part_o[at * D + lane * E + e] = o[e];
+    if (lane == 0) a.part_ml[at] = make_float2(m, l);
+  } else {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const size_t at = qi * D + lane * E + e;
+      if constexpr (DT == DT_F32) static_cast<float *>(a.out)[at] = o[e] * inv;
+      else static_cast<uint16_t *>(a.out)[at] = (uint16_t)round2<DT>(o[e] * inv, 0.f);
+    }
+  }
 }
 
 // the 16 queries' B operand; lanes of an absent column hold zeros
@@ -241,7 +330,7 @@ __device__ __forceinline__ float column_sum(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
-// element i of a lane's D / 4 output elements: product i % EP, row entry i / EP
+// a lane's D / 4 output elements (element i: product i % EP, row entry i / EP) of a row
 template <int DT, int D>
 __device__ __forceinline__ void store_output(uint8_t *row, int lane, const float (&x)[D / 4]) {
   if constexpr (DT == DT_F32) {

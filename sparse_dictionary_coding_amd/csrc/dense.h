@@ -46,12 +46,18 @@ struct AttendArgs {
   float scale;
   int32_t window, sinks;    // window: INT32_MAX where there is none
   int32_t splits;
-  float *part_o;            // [R][heads][splits][d]
-  float2 *part_ml;          // [R][heads][splits]
+  float *part_o;            // [queries][splits][d]: sum p v, not divided
+  float2 *part_ml;          // [queries][splits]: maximum (-inf: nothing visible), sum of p
 };
-// workgroups that share the length of a row's cache, at most
+// parts that a row's (attend_paged) or a block of columns' (attend_prompt) tokens are split into, at
+// most; `visible` bounds the tokens that one query sees
 int attend_paged_splits(int64_t R, int32_t kv_heads, int32_t group, int64_t visible);
+int attend_prompt_splits(int dtype, int64_t R, int64_t n, int32_t kv_heads, int32_t group,
+                         int64_t visible);
 hipError_t launch_attend_paged(int dtype, int d, const AttendArgs &a, hipStream_t stream);
 hipError_t launch_attend_prompt(int dtype, int d, const AttendArgs &a, hipStream_t stream);
+// joins the parts of `queries` queries (token times heads plus head) to the output
+hipError_t launch_attend_join(int dtype, int d, const AttendArgs &a, int64_t queries,
+                              hipStream_t stream);
 
 }  // namespace fadkv

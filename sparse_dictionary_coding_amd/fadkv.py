@@ -146,9 +146,12 @@ def lib() -> ctypes.CDLL:
         h.fadkv_attend_paged.restype = ctypes.c_int
         h.fadkv_attend_paged.argtypes = [P(fadkv_pages), ptr, i32, ptr, i64, ptr, i32,
                                          ctypes.c_float, i32, i32, i32, ptr, ptr, size, ptr]
+        h.fadkv_attend_prompt_workspace_bytes.restype = ctypes.c_int
+        h.fadkv_attend_prompt_workspace_bytes.argtypes = [P(fadkv_pages), i64, i64, i32, i32,
+                                                          P(size)]
         h.fadkv_attend_prompt.restype = ctypes.c_int
         h.fadkv_attend_prompt.argtypes = [P(fadkv_pages), ptr, i32, ptr, ptr, i64, ptr, i64, i32,
-                                          ctypes.c_float, i32, i32, ptr, ptr]
+                                          ctypes.c_float, i32, i32, i32, ptr, ptr, size, ptr]
         _lib_handle = h
     return _lib_handle
 
@@ -817,20 +820,40 @@ def fadkv_attend_paged(pages: Pages, table: torch.Tensor, lens: torch.Tensor, q:
     return out
 
 
+def fadkv_attend_prompt_workspace_bytes(pages: Pages, R: int, n: int, heads: int,
+                                        max_len: int) -> int:
+    out = ctypes.c_size_t(0)
+    st = lib().fadkv_attend_prompt_workspace_bytes(ctypes.byref(pages.c()), int(R), int(n),
+                                                   int(heads), int(max_len), ctypes.byref(out))
+    if st != FADKV_OK:
+        raise FadkvError("fadkv_attend_prompt_workspace_bytes", st)
+    return int(out.value)
+
+
 def fadkv_attend_prompt(pages: Pages, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
                         q: torch.Tensor, scale: float, window: int = 0, sinks: int = 0,
-                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                        max_len: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Causal attention of packed tokens q [n][heads][d]: tokens cu[r] .. cu[r+1] - 1 are the last
     of row r's lens[r] cached ones.  Returns (or fills) out [n][heads][d]; rows of out behind the
     last token stay as they were (undefined where out is allocated here)."""
     dev = _device_of(q, "q")
     if _elsewhere(dev, stream):
         with _on(dev, stream):
-            return fadkv_attend_prompt(pages, table, lens, cu, q, scale, window, sinks, out)
+            return fadkv_attend_prompt(pages, table, lens, cu, q, scale, window, sinks, max_len,
+                                       out, workspace)
     p, qp, tp, lp, op, out, n, heads, R, max_pages = _attend_args(pages, table, lens, q, out, dev)
     cp = _ptr(cu, "cu", _I32, (R + 1,), dev)
+    if max_len is None:
+        max_len = max_pages * p.page_size
+    if workspace is None:
+        need = fadkv_attend_prompt_workspace_bytes(pages, R, n, heads, max_len)
+        ws, need = (torch.empty(need, dtype=torch.uint8, device=q.device).data_ptr(), need) \
+            if need else (None, 0)
+    else:
+        ws, need = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
     st = lib().fadkv_attend_prompt(ctypes.byref(p), tp, max_pages, lp, cp, R, qp, n, heads, scale,
-                                   window, sinks, op, _raw_stream(dev))
+                                   window, sinks, max_len, op, ws, need, _raw_stream(dev))
     if st != FADKV_OK:
         raise FadkvError("fadkv_attend_prompt", st)
     return out

@@ -187,9 +187,10 @@ def _paged(pages=None, table=FAKE, max_pages=8, lens=FAKE, R=4, q=FAKE, heads=32
 
 
 def _prompt(pages=None, table=FAKE, max_pages=8, lens=FAKE, cu=FAKE, R=4, q=FAKE, n=20, heads=32,
-            scale=0.1, window=0, sinks=0, out=FAKE):
+            scale=0.1, window=0, sinks=0, max_len=100, out=FAKE, ws=FAKE, ws_bytes=1 << 40):
     return fadkv.lib().fadkv_attend_prompt(ctypes.byref(pages or _pages()), table, max_pages, lens,
-                                           cu, R, q, n, heads, scale, window, sinks, out, None)
+                                           cu, R, q, n, heads, scale, window, sinks, max_len, out,
+                                           ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("call", [_paged, _prompt])
@@ -222,3 +223,19 @@ def test_attend_prompt_refusals_of_its_own():
     assert _prompt(n=-1) == -3 and _prompt(n=(1 << 23) + 1) == -3
     assert _prompt(cu=None) == -1 and _prompt(cu=FAKE + 2) == -1
     assert _prompt(n=0, q=None, out=None) == 0
+    assert _prompt(max_len=0) == -3 and _prompt(max_len=129) == -3
+    out = ctypes.c_size_t(0)
+    f = fadkv.lib().fadkv_attend_prompt_workspace_bytes
+    assert f(ctypes.byref(_pages(k=None, v=None)), 1, 20, 32, 4096, ctypes.byref(out)) == 0
+    need = out.value
+    assert need > 0 and need % 256 == 0
+    long = dict(R=1, max_pages=256, max_len=4096)
+    assert _prompt(**long, ws_bytes=need - 1) == -4
+    assert _prompt(**long, ws=None) == -4 and _prompt(**long, ws=FAKE + 16) == -4
+    assert f(ctypes.byref(_pages()), 1, 20, 32, 0, ctypes.byref(out)) == -3
+    assert f(ctypes.byref(_pages()), 1, 20, 31, 10, ctypes.byref(out)) == -3
+    assert f(ctypes.byref(_pages()), 1, -1, 32, 10, ctypes.byref(out)) == -3
+    assert f(ctypes.byref(_pages()), 1, 20, 32, 10, None) == -1
+    # enough queries need no split, nor does a short cache
+    assert f(ctypes.byref(_pages()), 1, 4096, 32, 1 << 20, ctypes.byref(out)) == 0 and out.value == 0
+    assert f(ctypes.byref(_pages()), 1, 20, 32, 256, ctypes.byref(out)) == 0 and out.value == 0

@@ -153,7 +153,7 @@ NR = [
     ("f32", 4, 1, 1, 64, 16, True, True, 0.5, (1 << 30) + 7),
     ("bf16", 1, 32, 8, 128, 32, True, True, 1.0, 8191),
     ("f16", 3, 2, 1, 128, 0, False, True, 1.0, 0),
-    ("f32", 1030, 2, 1, 64, 48, False, False, 1.0, 3),       # four tokens a workgroup, odd end
+    ("f32", 1030, 2, 1, 64, 48, False, False, 1.0, 3),
     ("bf16", 1027, 6, 2, 128, 128, True, True, 1.0, 50),
     ("f16", 2, 65, 13, 64, 32, False, True, 1.0, 77),
 ]
@@ -226,6 +226,26 @@ def test_norm_rope_in_place_without_pages_and_empty():
     one[0, 1, 5] = float("nan")
     y = fadkv.fadkv_norm_rope(one, k[:1], v[:1], pos[:1], freqs, qw.to(DEV), kw.to(DEV))
     assert (y[0, 0] == 0).all() and y[0, 1].isnan().all() and (y[0, 2] == 0).all()
+
+
+@pytest.mark.parametrize("dt,n", [("f16", 9001), ("f32", 4600)])
+def test_norm_rope_large_batches_equal_small_ones(dt, n):
+    """Outputs stored around the caches (beyond 32 MB) are those of a small call, bit for bit."""
+    _banner(f"norm_rope {dt} n={n}")
+    x = torch.randn(n, 24, 128, device=DEV).to(TORCH[dt])
+    w = torch.ones(128, device=DEV).to(TORCH[dt])
+    freqs, _ = fadkv.fadkv_rope_freqs(128, 500000.0, device=DEV)
+    pos = torch.arange(n, device=DEV, dtype=torch.int32)
+    rows = torch.empty(2, 4, n, 128, dtype=TORCH[dt], device=DEV)
+
+    def call(a, b, kr, vr):
+        return fadkv.fadkv_norm_rope(x[a:b, :16], x[a:b, 16:20], x[a:b, 20:], pos[a:b], freqs, w, w,
+                                     k_rows=kr, v_rows=vr)
+    out = call(0, n, rows[0], rows[1])
+    for a in (0, n // 2, n - 7):
+        kr, vr = torch.empty(2, 4, 7, 128, dtype=TORCH[dt], device=DEV)
+        assert torch.equal(call(a, a + 7, kr, vr), out[a:a + 7])
+        assert torch.equal(kr, rows[0][:, a:a + 7]) and torch.equal(vr, rows[1][:, a:a + 7])
 
 
 # ---- attention ----------------------------------------------------------------------------------
@@ -389,7 +409,7 @@ def test_attend_paged_beyond_32_bits():
     assert torch.equal(pages.k[16999, :, 255], kvs[0]) and torch.equal(pages.v[16999, :, 255], kvs[0])
 
 
-def _check_prompt(dt, kv, group, d, page, cached, fresh, window=0, sinks=0, seed=0, pad=0, rows=None):
+def _check_prompt(dt, kv, group, d, page, cached, fresh, window=0, sinks=0, seed=0, pad=0):
     lens = np.asarray(cached) + np.asarray(fresh)
     pages, table = _cache(dt, kv, d, page, lens, seed=seed)
     cu = np.concatenate([[0], np.cumsum(fresh)])
@@ -398,7 +418,7 @@ def _check_prompt(dt, kv, group, d, page, cached, fresh, window=0, sinks=0, seed
     q = (2 * torch.randn(n + pad, kv * group, d, generator=g)).to(TORCH[dt])
     out = torch.full(q.shape, 9.0, dtype=TORCH[dt], device=DEV)
     scale = d ** -0.5
-    fadkv.fadkv_attend_prompt(pages, table, _i32(lens), _i32(cu), q.to(DEV), scale, window, sinks, out)
+    fadkv.fadkv_attend_prompt(pages, table, _i32(lens), _i32(cu), q.to(DEV), scale, window, sinks, out=out)
     torch.cuda.synchronize()
     got = _f64(out)
     assert (got[n:] == 9.0).all()
@@ -435,6 +455,66 @@ PROMPT = [
 def test_attend_prompt(dt, kv, group, d, page, cached, fresh, window, sinks, pad):
     _banner(f"prompt {dt} kv={kv}x{group} d={d} page={page} {cached}+{fresh} window={window}/{sinks}")
     _check_prompt(dt, kv, group, d, page, cached, fresh, window, sinks, seed=d + page, pad=pad)
+
+
+LONG = [
+    # few queries over long caches: split over the length
+    ("f16", 1, 4, 128, 16, [5000], [3], 0, 0, 2),
+    ("bf16", 2, 1, 64, 64, [3000, 0, 900], [20, 5, 1], 0, 0, 0),
+    ("f32", 1, 2, 128, 16, [2500, 64], [17, 9], 0, 0, 1),
+    ("bf16", 1, 8, 128, 32, [4000, 700], [33, 2], 1500, 5, 0),
+    ("f32", 2, 3, 64, 16, [1500], [40], 700, 64, 0),
+    ("f16", 1, 2, 64, 16, [0, 2000], [300, 0], 0, 0, 3),
+]
+
+
+@pytest.mark.parametrize("dt,kv,group,d,page,cached,fresh,window,sinks,pad", LONG)
+def test_attend_prompt_split(dt, kv, group, d, page, cached, fresh, window, sinks, pad):
+    _banner(f"prompt split {dt} kv={kv}x{group} d={d} {cached}+{fresh} window={window}/{sinks}")
+    _check_prompt(dt, kv, group, d, page, cached, fresh, window, sinks, seed=d + page, pad=pad)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("cached,fresh,window,sinks", [(0, 200, 0, 0), (2000, 10, 0, 0), (100, 150, 60, 7)])
+def test_attend_prompt_keeps_what_is_not_seen_away(dt, cached, fresh, window, sinks):
+    """Infinities and NaN in keys and values of some tokens reach the queries that see them, by the
+    formula's rules, and leave the others as they are without them."""
+    _banner(f"prompt non-finite {dt} {cached}+{fresh} window={window}/{sinks}")
+    n, d = cached + fresh, 64
+    pages, table = _cache(dt, 1, d, 16, [n], seed=8)
+    q = torch.randn(fresh, 2, d, device=DEV).to(TORCH[dt])
+    args = (_i32([n]), _i32([0, fresh]), q, d ** -0.5, window, sinks)
+    clean = fadkv.fadkv_attend_prompt(pages, table, *args)
+    bad = {n - 5: float("nan"), n - fresh // 2: float("inf"), 3: float("-inf")}
+    for t, x in bad.items():
+        pages.v[int(table[0, t // 16]), 0, t % 16, 10] = x
+        pages.k[int(table[0, t // 16]), 0, t % 16, :] = float("nan") if x != x else 0.0
+    got = fadkv.fadkv_attend_prompt(pages, table, *args)
+    zero = [t for t, x in bad.items() if x == x]           # tokens whose keys became zeros
+    for i in range(fresh):
+        pos = n - fresh + i
+        seen = [t for t in bad if dense_oracle.visible(pos, t, window, sinks)]
+        if not seen:       # another path may take the block: the same up to a few roundings
+            e = 2.0 ** -6 if dt == "bf16" else (2.0 ** -9 if dt == "f16" else 1e-5)
+            torch.testing.assert_close(got[i].float(), clean[i].float(), rtol=e, atol=e)
+        elif any(bad[t] != bad[t] for t in seen):
+            assert got[i].isnan().all()
+        else:
+            vals = {bad[t] for t in seen}
+            assert (got[i, :, 10].isnan() if len(vals) == 2 else got[i, :, 10] == vals.pop()).all()
+            keep = [c for c in range(d) if c != 10]
+            assert got[i][:, keep].isfinite().all()
+    assert zero
+
+
+def test_attend_prompt_large_outputs_of_one_call_equal_small_ones():
+    """A query's result does not depend on which others are in the call (the same tiles, one split)."""
+    _banner("prompt of one call and of two")
+    pages, table = _cache("bf16", 8, 64, 64, [4096], seed=2)
+    q = torch.randn(4096, 16, 64, device=DEV).bfloat16()
+    whole = fadkv.fadkv_attend_prompt(pages, table, _i32([4096]), _i32([0, 4096]), q, 0.125)
+    part = fadkv.fadkv_attend_prompt(pages, table, _i32([4096]), _i32([0, 2048]), q[2048:].contiguous(), 0.125)
+    torch.testing.assert_close(whole[2048:].float(), part.float(), rtol=2.0 ** -6, atol=2.0 ** -8)
 
 
 def test_attend_prompt_many_rows():
