@@ -28,42 +28,38 @@ constexpr int PM_FILL = 512;
 constexpr int PR_LEAST = 64;
 constexpr int PM_LEAST = 256;
 
-// Workgroup -> (row, block of `per` columns): rows in order, ceil(tokens * group / per) blocks each.
-// Every lane of the wave gets the answer; row = R where the workgroup has none.
+// Workgroup -> (row, block of `per` columns).  Row r's blocks are numbered from
+// floor(cu[r] * group / per) + r, which leaves room for all of them (ceil(x) <= floor(b) - floor(a) + 1
+// for b - a = x) and, at most, one number without a block; so the row of a number is found by a
+// search in cu, 64 rows a step, without adding up the rows before it.  The answer is the
+// same for all lanes; tokens = 0 where the number has no block.
 struct RowBlock {
   int row, block, begin, tokens;   // first packed token and token count of the row
 };
 
+__device__ __forceinline__ int64_t clamped_cu(const AttendArgs &a, int r) {
+  const int64_t c = a.cu[r];
+  return c < 0 ? 0 : (c > a.n ? a.n : c);
+}
+
 __device__ __forceinline__ RowBlock find_row(const AttendArgs &a, int64_t blk, int per, int lane) {
-  RowBlock rb = {a.R, 0, 0, 0};
-  int64_t before = 0;
-  for (int r0 = 0; r0 < a.R; r0 += 64) {
-    const int r = r0 + lane;
-    int64_t b = 0, e = 0;
-    if (r < a.R) {
-      b = a.cu[r];
-      e = a.cu[r + 1];
-      b = b < 0 ? 0 : (b > a.n ? a.n : b);
-      e = e < b ? b : (e > a.n ? a.n : e);
-    }
-    const int64_t mine = ((e - b) * a.group + per - 1) / per;
-    int64_t through = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t u = __shfl_up((long long)through, o, 64);
-      if (lane >= o) through += u;
-    }
-    through += before;
-    const unsigned long long hit = __ballot(blk < through);
-    if (hit) {
-      const int src = __builtin_ctzll(hit);   // the same for all lanes: scalar registers from here
-      rb.row = r0 + src;
-      rb.block = __builtin_amdgcn_readlane((int)(blk - (through - mine)), src);
-      rb.begin = __builtin_amdgcn_readlane((int)b, src);
-      rb.tokens = __builtin_amdgcn_readlane((int)(e - b), src);
-      return rb;
-    }
-    before = __shfl((long long)through, 63, 64);
+  int lo = 0, len = a.R;   // the row is in [lo, lo + len)
+  while (len > 1) {
+    const int step = (len + 63) >> 6;
+    const int r = lo + lane * step;
+    const bool at = lane * step < len && clamped_cu(a, r) * a.group / per + r <= blk;
+    const unsigned long long hit = __ballot(at);
+    const int k = hit ? 63 - __builtin_clzll(hit) : 0;
+    lo += k * step;
+    len = len - k * step < step ? len - k * step : step;
+  }
+  RowBlock rb = {lo, 0, 0, 0};
+  const int64_t b = clamped_cu(a, lo), e = clamped_cu(a, lo + 1);
+  const int64_t block = blk - (b * a.group / per + lo);
+  if (e > b && block >= 0 && block < ((e - b) * a.group + per - 1) / per) {
+    rb.block = __builtin_amdgcn_readfirstlane((int)block);
+    rb.begin = __builtin_amdgcn_readfirstlane((int)b);
+    rb.tokens = __builtin_amdgcn_readfirstlane((int)(e - b));
   }
   return rb;
 }
@@ -112,7 +108,7 @@ __global__ __launch_bounds__(64 * PR_WAVES) void attend_prompt_kernel(AttendArgs
   const int split = SPLIT ? (int)(blk % a.splits) : 0;
   if (SPLIT) blk /= a.splits;
   const RowBlock rb = find_row(a, blk, 16 * PR_WAVES, lane);
-  if (rb.row >= a.R) return;
+  if (rb.tokens == 0) return;
   const int heads = a.kv_heads * a.group;
   const int64_t room = (int64_t)a.max_pages << a.page_shift;
   int len = a.lens[rb.row];
@@ -248,7 +244,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   const int split = SPLIT ? (int)(blk % a.splits) : 0;
   if (SPLIT) blk /= a.splits;
   RowBlock rb = find_row(a, blk, 32 * WAVES, lane);
-  if (rb.row >= a.R) return;
+  if (rb.tokens == 0) return;
   const int heads = a.kv_heads * a.group;
   const int64_t cols = (int64_t)rb.tokens * a.group;
   // the blocks with the most tokens first
@@ -348,18 +344,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
       const int r = row0 + lane / LPR;
       const bool seen = at >= 0 && sees(any, a.sinks, t0 + r);
       uint4 *row = reinterpret_cast<uint4 *>(&s_kv[stage][1][r * ROWB]);
-      bool bad = false;
+      uint32_t bad = 0;
 #pragma unroll
       for (int c = 0; c < CPR; c += LPR) {
         uint4 *at16 = row + c + lane % LPR;
         if (seen) {
           const uint4 w = *at16;
-          bad |= odd_value<DT>(w.x) || odd_value<DT>(w.y) || odd_value<DT>(w.z) || odd_value<DT>(w.w);
+          bad |= odd_value<DT>(w.x) | odd_value<DT>(w.y) | odd_value<DT>(w.z) | odd_value<DT>(w.w);
         } else {
           *at16 = make_uint4(0, 0, 0, 0);
         }
       }
-      if (__any(bad) && lane == 0) s_miss[stage][grp] = 2;
+      if (__any(bad != 0) && lane == 0) s_miss[stage][grp] = 2;
     }
     tile::wait_lds();
   };
@@ -424,7 +420,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
     const int64_t at_now = at_k;             // tile i + 1
     at_k = group_offset(i + 2);
     const int t0 = start_of(i);
-    if (i + 1 < count) copy_values(stage ^ 1, at_now);
     if (i + 2 < count) copy_keys(stage, at_k);
     const bool full = !(gone[0] | gone[1] | gone[2] | gone[3]) && t0 + PT <= all.hi &&
                       (t0 >= all.lo || t0 + PT <= a.sinks);
@@ -455,6 +450,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[b][e] *= keep;
     }
+    if (i + 1 < count) copy_values(stage ^ 1, at_now);
     float16_t next[2];
     scores(stage ^ 1, next);   // behind the last tile: of old keys, not used
     const uint8_t *vt = s_kv[stage][1];
@@ -530,15 +526,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
     }
 }
 
-// Columns per workgroup; at most one started block more per row than the columns fill.
-static int64_t prompt_blocks(int dtype, int64_t R, int64_t n, int32_t group) {
-  const int per = dtype == DT_F32 ? 16 * PR_WAVES : 32 * PM_WAVES;
-  return n * group / per + (R < n ? R : n);
-}
+// columns per workgroup
+static int prompt_columns(int dtype) { return dtype == DT_F32 ? 16 * PR_WAVES : 32 * PM_WAVES; }
 
 int attend_prompt_splits(int dtype, int64_t R, int64_t n, int32_t kv_heads, int32_t group,
                          int64_t visible) {
-  const int64_t wgs = prompt_blocks(dtype, R, n, group) * kv_heads;
+  const int64_t wgs = (n * group / prompt_columns(dtype) + (R < n ? R : n)) * kv_heads;
   int64_t s = wgs > 0 ? (PM_FILL + wgs - 1) / wgs : 1;
   const int64_t least = dtype == DT_F32 ? PR_LEAST : PM_LEAST;
   const int64_t most = (visible + least - 1) / least;
@@ -548,7 +541,8 @@ int attend_prompt_splits(int dtype, int64_t R, int64_t n, int32_t kv_heads, int3
 
 template <int DT, int D>
 static hipError_t attend_prompt_run(const AttendArgs &a, hipStream_t stream) {
-  const int64_t wgs = prompt_blocks(DT, a.R, a.n, a.group) * a.kv_heads;
+  // the blocks' numbers end below floor(n * group / columns) + R (find_row)
+  const int64_t wgs = (a.n * a.group / prompt_columns(DT) + a.R) * a.kv_heads;
   const dim3 grid((unsigned)(wgs * a.splits));
   if constexpr (DT == DT_F32) {
     const dim3 block(64 * PR_WAVES);

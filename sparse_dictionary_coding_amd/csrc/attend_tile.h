@@ -152,11 +152,12 @@ template <int DT, int D> struct KvTile {
   }
 };
 
-// an infinity or NaN among the values of a 32-bit word (two in the 16-bit types)
-template <int DT> __device__ __forceinline__ bool odd_value(uint32_t w) {
-  constexpr uint32_t E = DT == DT_F32 ? 0x7f800000u : (DT == DT_F16 ? 0x7c00u : 0x7f80u);
-  if constexpr (DT == DT_F32) return (w & E) == E;
-  else return (w & E) == E || ((w >> 16) & E) == E;
+// Not 0 where a value of the 32-bit word (two in the 16-bit types) is an infinity or NaN: one added
+// to an exponent of all ones carries into the sign's place.
+template <int DT> __device__ __forceinline__ uint32_t odd_value(uint32_t w) {
+  if constexpr (DT == DT_F32) return ((w & 0x7f800000u) + 0x00800000u) & 0x80000000u;
+  else if constexpr (DT == DT_F16) return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+  else return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
 // One tile against the wave's 16 columns.  `whole`: every column sees all 32 tokens (uniform).
@@ -191,12 +192,12 @@ __device__ __forceinline__ bool attend_tile(KvTile<DT, D> &kv, const uint4 (&q)[
       }
     }
     if constexpr (MIXED) {
-      bool bad = false;
+      uint32_t bad = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int c = 0; c < T::VW; ++c) bad |= odd_value<DT>(kv.v[j][c]);
-      if (__any(bad)) return false;
+      if (__any(bad != 0)) return false;
     }
   }
   float top = z[0];
