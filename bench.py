@@ -46,12 +46,14 @@ def parse():
     ap.add_argument("--no-prefill", action="store_true",
                     help="skip the 3B prefill measurement added to the default decode line")
     ap.add_argument("--cpu-seconds", type=float, default=12.0)
-    ap.add_argument("--path", default="encode", choices=["encode", "attend", "growth", "omp"],
+    ap.add_argument("--path", default="encode", choices=["encode", "attend", "growth", "omp", "dense"],
                     help="encode: the encoder hot path (default); attend: decode attention of "
                          "one layer over the sparse codes; growth: a long run committed both "
                          "fixed-size and append-only, with the dictionary-size trace; omp: "
                          "coding cost of GM and PL relative to the full-dictionary greedy "
-                         "yardstick, and the pool recall of the yardstick's atoms")
+                         "yardstick, and the pool recall of the yardstick's atoms; dense: one "
+                         "layer's decode step on the paged dense cache, from the projection's "
+                         "heads to attention and the new tokens' codes")
     ap.add_argument("--growth-steps", type=int, default=0,
                     help="decode steps of the long run (--path growth; default: the workload's)")
     ap.add_argument("--trace-out", default="", help="per-step trace as JSON (--path growth)")
@@ -60,7 +62,7 @@ def parse():
                          "synthetic prefill uses every atom a few times, so with the library's "
                          "default of 1 no atom is inactive afterwards; 64 leaves about 12%% of "
                          "them inactive")
-    ap.add_argument("--tokens", type=int, default=2048, help="cached tokens per row (--path attend)")
+    ap.add_argument("--tokens", type=int, default=2048, help="cached tokens per row (--path attend, dense)")
     ap.add_argument("--copy-calibration-mib", type=int, default=0,
                     help="before timing, copy a buffer of this many MiB three times (a plain "
                          "device copy of known size, for scaling memory-traffic counters)")
@@ -234,6 +236,99 @@ def bench_attend(args):
                                "sample": f"{rows} of {R} rows x {G} queries x {T} tokens "
                                          f"(NumPy fp64, Python loops), {dt:.1f} s"}
     print(json.dumps(res), flush=True)
+
+
+def bench_dense(args):
+    """One layer's decode step on the paged dense cache, replayed as one HIP graph: page
+    bookkeeping, norm and rotation with the cache write, attention over `--tokens` cached tokens
+    per sequence, and the codes of the new keys and values, whose rows the second call leaves in
+    the encoder's order.  Prints one JSON line; `value` is new tokens per second, `stages` the
+    HIP-event times of the four calls launched one by one."""
+    import torch
+
+    from sparse_dictionary_coding_amd import fadkv, synth
+
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    w = synth.WORKLOADS[args.workload]
+    kv, seqs, d, heads, page = w.kv_heads, w.seqs, w.d, 4 * w.kv_heads, 16
+    steps = 2 * args.steps + args.warmup + 2           # every step appends a token
+    width = -(-(args.tokens + steps) // page)
+    pt = fadkv.PageTable.empty(seqs, width, seqs * width, page, dev)
+    gen = synth.SyntheticKV(w, device=dev, num_dicts=2)
+    atoms = gen.atoms()                                # dictionary 0 = keys, 1 = values
+    dt = atoms.dtype
+    pages = fadkv.Pages.empty(seqs * width, kv, page, d, dt, dev)
+    pages.k.normal_()
+    pages.v.normal_()
+    freqs, mscale = fadkv.fadkv_rope_freqs(d, 500000.0, "bands", 8.0, 1.0, 4.0, 8192, device=dev)
+    wq, wk = (torch.ones(d, dtype=dt, device=dev) for _ in range(2))
+    qkv = torch.randn(seqs, heads + 2 * kv, d, device=dev).to(dt)
+    q, k, v = qkv[:, :heads], qkv[:, heads:heads + kv], qkv[:, heads + kv:]
+    q_out, out = (torch.empty(seqs, heads, d, dtype=dt, device=dev) for _ in range(2))
+    X = torch.empty(2, kv * seqs, d, dtype=dt, device=dev)
+    p = fadkv.Params(n=w.n, s=w.s, select=args.select)
+    codes = fadkv.Codes.empty(2, kv * seqs, w.s, dev)
+    ws = fadkv.make_workspace(atoms, p, kv * seqs)
+    aws = torch.empty(max(1, fadkv.fadkv_attend_paged_workspace_bytes(pages, seqs, heads, width * page)),
+                      dtype=torch.uint8, device=dev)
+    fadkv.fadkv_pages_advance(pt, torch.full((seqs,), args.tokens, dtype=torch.int32, device=dev),
+                              out=fadkv.PageStep.empty(pt, seqs * args.tokens, in_place=True))
+    one = torch.ones(seqs, dtype=torch.int32, device=dev)
+    ps = fadkv.PageStep.empty(pt, seqs, in_place=True)
+    scale = float(d) ** -0.5
+    stages = {
+        "pages_advance": lambda: fadkv.fadkv_pages_advance(pt, one, out=ps),
+        "norm_rope": lambda: fadkv.fadkv_norm_rope(
+            q, k, v, ps.positions, freqs, wq, wk, mscale=mscale, pages=pages, slots=ps.slots,
+            q_out=q_out, k_rows=X[0].view(kv, seqs, d), v_rows=X[1].view(kv, seqs, d)),
+        "attend_paged": lambda: fadkv.fadkv_attend_paged(pages, pt.table, pt.lens, q_out, scale,
+                                                         out=out, workspace=aws),
+        "encode": lambda: fadkv.fadkv_encode(atoms, X, p, out=codes, workspace=ws),
+    }
+
+    def step():
+        for f in stages.values():
+            f()
+    step()
+    ms = dict.fromkeys(stages, 0.0)
+    for _ in range(args.steps):
+        for name, f in stages.items():
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            f()
+            b.record()
+            torch.cuda.synchronize()
+            ms[name] += a.elapsed_time(b) / args.steps
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(args.warmup):
+        graph.replay()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    for _ in range(args.steps):
+        graph.replay()
+    torch.cuda.synchronize()
+    wall = time.perf_counter() - t0
+    assert int(pt.lens.min()) == args.tokens + 1 + 2 * args.steps + args.warmup
+    kv_bytes = 2 * int(pt.lens.sum()) * kv * d * atoms.element_size()
+    gbs = kv_bytes / (ms["attend_paged"] * 1e-3) / 1e9
+    print(json.dumps({
+        "metric": "decode step of one layer on the paged dense cache: new tokens/s",
+        "value": seqs * args.steps / wall, "unit": "tokens/s", "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": wall * 1e3 / args.steps, "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None, "dtype": w.dtype, "data": "synthetic",
+        "config": {"workload": f"{w.name} dense cache, one layer", "sequences": seqs,
+                   "query_heads": heads, "kv_heads": kv, "d": d, "tokens": args.tokens,
+                   "page_size": page, "N": w.N, "n": w.n, "s": w.s, "select": args.select,
+                   "launch": "hip graph per step"},
+        "stages": {name: {"ms": t} for name, t in ms.items()},
+        "roofline": {"kernel": "attend_paged_kernel + attend_join_kernel", "bound": "hbm",
+                     "achieved": gbs, "peak": HBM_PEAK_GBS, "unit": "GB/s",
+                     "frac": gbs / HBM_PEAK_GBS, "traffic": None},
+        "kv_bytes": kv_bytes,
+    }), flush=True)
 
 
 def bench_growth(args):
@@ -744,6 +839,9 @@ def main():
         sys.exit(2)
     if args.path == "attend":
         bench_attend(args)
+        return
+    if args.path == "dense":
+        bench_dense(args)
         return
     if args.path == "growth":
         bench_growth(args)

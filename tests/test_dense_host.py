@@ -4,12 +4,17 @@ every check returns before a HIP call)."""
 import ctypes
 import math
 import os
+import re
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
 
 from oracle import dense_oracle
-from sparse_dictionary_coding_amd import fadkv
+from sparse_dictionary_coding_amd import build, fadkv
+
+HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 
 pytestmark = pytest.mark.skipif(not os.path.exists(fadkv.LIB_PATH),
                                 reason="libfadkv.so not built (run __graft_entry__.build())")
@@ -239,3 +244,30 @@ def test_attend_prompt_refusals_of_its_own():
     # enough queries need no split, nor does a short cache
     assert f(ctypes.byref(_pages()), 1, 4096, 32, 1 << 20, ctypes.byref(out)) == 0 and out.value == 0
     assert f(ctypes.byref(_pages()), 1, 20, 32, 256, ctypes.byref(out)) == 0 and out.value == 0
+
+
+# ---- generated code -----------------------------------------------------------------------------
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not available")
+def test_prompt_kernels_use_m0_for_their_copies_alone(tmp_path):
+    """The prompt attention writes M0 in assembly for its copies into LDS, which is sound while the
+    compiler keeps nothing there; and no kernel of the dense cache has packed fp32 arithmetic."""
+    for name in ("attend_prompt.hip", "attend_paged.hip", "norm_rope.hip", "pages.hip"):
+        out = tmp_path / (name + ".s")
+        cmd = [HIPCC, *build.HIPCC_FLAGS, f"-I{build.INCLUDE}", f"-I{build.CSRC}",
+               "--cuda-device-only", "-S", os.path.join(build.CSRC, name), "-o", str(out)]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
+        lines = [ln.strip() for ln in out.read_text().splitlines()]
+        assert not [ln for ln in lines if re.match(r"v_pk_(add|mul|fma)_f32", ln)]
+        assert not [ln for ln in lines if re.match(r"scratch_(load|store)", ln)], name
+        if name != "attend_prompt.hip":
+            continue
+        copies = 0
+        for i, ln in enumerate(lines):
+            if ln.startswith(";") or not re.search(r"\bm0\b", ln):
+                continue
+            assert re.fullmatch(r"s_mov_b32 m0, s\d+", ln), f"unexpected M0 use: {ln}"
+            assert lines[i + 1] == "s_nop 0", lines[i + 1]
+            assert lines[i + 2].startswith("global_load_lds_dwordx4 "), lines[i + 2]
+            copies += 1
+        assert copies > 0
