@@ -110,7 +110,7 @@ __global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendAr
   // loads wait for no table entry; and a tile is loaded while the one before it is worked on.
   const auto start_of = [&](int i) { return (i < tl.first ? i : tl.from + i - tl.first) << 5; };
   int ids0 = -1, ids1 = -1;
-  const auto fetch = [&](KvTile<DT, D> &kv, int i) {
+  const auto fetch = [&](KvTile<DT, D, true> &kv, int i) {
     const int k = (i - i0) / AP_WAVES;   // the wave's tile number
     if ((k & 63) == 0) {
       const int mine = i + lane * AP_WAVES;
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendAr
   };
   AttState<DT, D> st;
   st.clear();
-  const auto attend = [&](KvTile<DT, D> &kv, int i) {
+  const auto attend = [&](KvTile<DT, D, true> &kv, int i) {
     const int t0 = start_of(i);
     const bool whole = kv.there[0] && kv.there[1] && t0 + 32 <= see.hi &&
                        (t0 >= see.lo || t0 + 32 <= a.sinks);
@@ -130,13 +130,13 @@ __global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendAr
   };
   int i = i0 + wave;
   if constexpr (DT == DT_F32) {   // two tiles of fp32 do not fit the registers of two waves a SIMD
-    KvTile<DT, D> kv;
+    KvTile<DT, D, true> kv;
     for (; i < i1; i += AP_WAVES) {
       fetch(kv, i);
       attend(kv, i);
     }
   } else {
-    KvTile<DT, D> even, odd;
+    KvTile<DT, D, true> even, odd;
     if (i < i1) fetch(even, i);
     while (i < i1) {
       if (i + AP_WAVES < i1) fetch(odd, i + AP_WAVES);

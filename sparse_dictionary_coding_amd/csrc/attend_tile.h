@@ -105,8 +105,17 @@ template <int DT, int D> struct AttState {
   }
 };
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// ONCE: what is loaded is not read again soon and leaves the caches to others
+template <bool ONCE, class T> __device__ __forceinline__ T load_vec(const void *p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(static_cast<const T *>(p));
+  else return *static_cast<const T *>(p);
+}
+
 // keys and values of 32 tokens in registers
-template <int DT, int D> struct KvTile {
+template <int DT, int D, bool ONCE> struct KvTile {
   uint4 k[2][AttTile<DT, D>::CH];
   uint32_t v[8][AttTile<DT, D>::VW];
   bool there[2];
@@ -121,22 +130,24 @@ template <int DT, int D> struct KvTile {
       const int64_t at = group_at<T::ROWB>(pv, a ? id1 : id0, t0 + 16 * a);
       there[a] = at >= 0;
       if (there[a]) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(pv.k + at + (size_t)r * T::ROWB);
+        const u32x4_t *src = reinterpret_cast<const u32x4_t *>(pv.k + at + (size_t)r * T::ROWB);
 #pragma unroll
-        for (int i = 0; i < T::CH; ++i) k[a][i] = src[4 * i + g];
+        for (int i = 0; i < T::CH; ++i)
+          k[a][i] = __builtin_bit_cast(uint4, load_vec<ONCE, u32x4_t>(src + 4 * i + g));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t *row =
               reinterpret_cast<const uint32_t *>(pv.v + at + (size_t)(4 * g + e) * T::ROWB) + r * T::VW;
           uint32_t *dst = v[4 * a + e];
           if constexpr (T::VW == 2) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(row);
-            dst[0] = w.x; dst[1] = w.y;
+            const u32x2_t w = load_vec<ONCE, u32x2_t>(row);
+            dst[0] = w[0]; dst[1] = w[1];
           } else {
 #pragma unroll
             for (int c = 0; c < T::VW / 4; ++c) {
-              const uint4 w = reinterpret_cast<const uint4 *>(row)[c];
-              dst[4 * c] = w.x; dst[4 * c + 1] = w.y; dst[4 * c + 2] = w.z; dst[4 * c + 3] = w.w;
+              const u32x4_t w = load_vec<ONCE, u32x4_t>(row + 4 * c);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) dst[4 * c + x] = w[x];
             }
           }
         }
@@ -164,8 +175,8 @@ template <int DT> __device__ __forceinline__ uint32_t odd_value(uint32_t w) {
 // Tokens that no column sees are zeroed in v: p = 0 does not undo an infinity or NaN there.  Where
 // the columns see different tokens (MIXED) the same holds for a token that some of them see: then
 // nothing is done and the answer is false (attend_column does such blocks).
-template <int DT, int D, bool MIXED>
-__device__ __forceinline__ bool attend_tile(KvTile<DT, D> &kv, const uint4 (&q)[AttTile<DT, D>::CH],
+template <int DT, int D, bool MIXED, bool ONCE>
+__device__ __forceinline__ bool attend_tile(KvTile<DT, D, ONCE> &kv, const uint4 (&q)[AttTile<DT, D>::CH],
                                             int t0, bool whole, const Visible &col,
                                             const Visible &any, int sinks, float scale2, int lane,
                                             AttState<DT, D> &st) {

@@ -83,15 +83,19 @@ template <int W> __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-template <int DT> __device__ __forceinline__ Pack8<DT> load8(const uint8_t *row, int lane) {
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+template <int DT>
+__device__ __forceinline__ Pack8<DT> load8(const uint8_t *row, int lane) {
   Pack8<DT> p;
-  const uint4 *src = reinterpret_cast<const uint4 *>(row) + lane * (DT == DT_F32 ? 2 : 1);
-  p.w[0] = src[0];
-  if constexpr (DT == DT_F32) p.w[1] = src[1];
+  const u32x4_t *src = reinterpret_cast<const u32x4_t *>(row) + lane * (DT == DT_F32 ? 2 : 1);
+#pragma unroll
+  for (int i = 0; i < (DT == DT_F32 ? 2 : 1); ++i) {
+    const u32x4_t v = src[i];
+    p.w[i] = make_uint4(v[0], v[1], v[2], v[3]);
+  }
   return p;
 }
-
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 template <int DT, bool STREAM>
 __device__ __forceinline__ void store8(uint8_t *row, int lane, const Pack8<DT> &p) {
