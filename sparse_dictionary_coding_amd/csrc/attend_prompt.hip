@@ -424,13 +424,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
     const bool full = !(gone[0] | gone[1] | gone[2] | gone[3]) && t0 + PT <= all.hi &&
                       (t0 >= all.lo || t0 + PT <= a.sinks);
     if (!full) {
+      // against offsets from the lane's first token, which leaves constants on this side
+      const int at = t0 + 4 * h;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int g = 0; g < 4; ++g) {
+        const Visible c = {see.lo - at, gone[g] ? -1 : see.hi - at};
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int k = 32 * kb + 8 * (e >> 2) + (e & 3);   // + 4 h
-          if (gone[k >> 4] || !sees(see, a.sinks, t0 + k + 4 * h)) s[kb][e] = -__builtin_inff();
+        for (int e = 0; e < 8; ++e) {
+          const bool seen = sees(c, a.sinks - at, 16 * g + 8 * (e >> 2) + (e & 3));
+          s[g >> 1][8 * (g & 1) + e] = seen ? s[g >> 1][8 * (g & 1) + e] : -__builtin_inff();
         }
+      }
     }
     float top = s[0][0];
 #pragma unroll

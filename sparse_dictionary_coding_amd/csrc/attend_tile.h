@@ -89,8 +89,9 @@ struct Visible {
   int lo, hi;
 };
 
+// (without branches)
 __device__ __forceinline__ bool sees(const Visible &s, int sinks, int t) {
-  return t < s.hi && (t >= s.lo || t < sinks);
+  return (t < s.hi) & ((t >= s.lo) | (t < sinks));
 }
 
 template <int DT, int D> struct AttState {
@@ -195,12 +196,14 @@ __device__ __forceinline__ bool attend_tile(KvTile<DT, D, ONCE> &kv, const uint4
   if (!whole) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
-      if (!kv.there[j >> 2] || !sees(col, sinks, t)) z[j] = -__builtin_inff();
-      if (!sees(any, sinks, t)) {
+      // against offsets from the lane's first token, which leaves constants on this side
+      const int k = 16 * (j >> 2) + (j & 3), at = t0 + 4 * g;
+      const Visible c = {col.lo - at, kv.there[j >> 2] ? col.hi - at : -1};
+      const Visible a = {any.lo - at, any.hi - at};
+      z[j] = sees(c, sinks - at, k) ? z[j] : -__builtin_inff();
+      const bool used = sees(a, sinks - at, k);
 #pragma unroll
-        for (int c = 0; c < T::VW; ++c) kv.v[j][c] = 0;
-      }
+      for (int w = 0; w < T::VW; ++w) kv.v[j][w] = used ? kv.v[j][w] : 0;
     }
     if constexpr (MIXED) {
       uint32_t bad = 0;
