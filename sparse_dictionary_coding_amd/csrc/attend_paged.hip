@@ -19,13 +19,15 @@ constexpr int AP_FILL = 512;      // workgroups that are resident at once: two o
 constexpr int AP_ROWS = 4;        // splits of a row of several
 constexpr int AP_LEAST = 256;     // tokens below which a share is not cut further
 constexpr int AP_JOIN = 4;        // waves that join a query's splits
+constexpr int AP_FEW = 8;         // splits that one thread joins,
+constexpr int AP_MANY = 4096;     // where there are more queries than this
 
 }  // namespace
 
 // As many splits as fill the chip in one round (measured at one row of 131072 tokens, 8 kv heads of
-// 128 in bf16: 512 workgroups 102 us, 1024 105, 2048 111), but four where there are several rows, so
-// that the end does not wait for the longest row (64 rows of 1 to 4096 tokens: four splits 115
-// us, one 120).
+// 128 in bf16: 512 workgroups 92 us, 1024 99, 2048 111), but four where there are several rows, so
+// that the end does not wait for the longest row (64 rows of 1 to 4096 tokens in fp16: four splits
+// 108 us, one 123).
 int attend_paged_splits(int64_t R, int32_t kv_heads, int32_t group, int64_t visible) {
   const int64_t wgs = R * kv_heads * ((group + 15) / 16);
   int64_t s = wgs > 0 ? (AP_FILL + wgs - 1) / wgs : 1;
@@ -260,18 +262,68 @@ __global__ __launch_bounds__(64 * AP_JOIN) void attend_join_kernel(AttendArgs a)
     static_cast<uint32_t *>(a.out)[qi * (D / 2) + threadIdx.x] = round2<DT>(y[0] * inv, y[1] * inv);
 }
 
+// The same for few splits: D / 4 threads per query, each four elements of it
+template <int DT, int D>
+__global__ __launch_bounds__(256) void attend_join_few_kernel(AttendArgs a, int64_t queries) {
+  constexpr int T = D / 4;
+  const int64_t qi = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
+  const int d4 = threadIdx.x % T;
+  if (qi >= queries) return;
+  if (a.cu) {
+    const int64_t tok = qi / (a.kv_heads * a.group);
+    if (tok < a.cu[0] || tok >= a.cu[a.R]) return;
+  }
+  const float2 *ml = a.part_ml + qi * a.splits;
+  const float4 *po = reinterpret_cast<const float4 *>(a.part_o + qi * a.splits * D) + d4;
+  float m = -__builtin_inff();
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[s].x);
+  const float base = m == -__builtin_inff() ? 0.f : m;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 x = ml[s];
+    if (x.x == -__builtin_inff() && x.y == 0.f) continue;
+    const float f = __builtin_amdgcn_exp2f(x.x - base);
+    const float4 v = po[(size_t)s * T];
+    sum = fmaf(x.y, f, sum);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if constexpr (DT == DT_F32)
+    static_cast<float4 *>(a.out)[qi * T + d4] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  else
+    static_cast<uint2 *>(a.out)[qi * T + d4] =
+        make_uint2(round2<DT>(o.x * inv, o.y * inv), round2<DT>(o.z * inv, o.w * inv));
+}
+
+template <int DT, int D>
+static void attend_join_run(const AttendArgs &a, int64_t queries, hipStream_t stream) {
+  constexpr int PER = 256 / (D / 4);
+  // A workgroup per query is the shorter chain (512 queries of four splits: 3.9 us against 5.4),
+  // until there are more than the chip takes at once (16384 queries of two splits: 18 us against
+  // 4.8).
+  if (a.splits <= AP_FEW && queries > AP_MANY)
+    hipLaunchKernelGGL((attend_join_few_kernel<DT, D>), dim3((unsigned)((queries + PER - 1) / PER)),
+                       dim3(256), 0, stream, a, queries);
+  else
+    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3((unsigned)queries), dim3(64 * AP_JOIN), 0,
+                       stream, a);
+}
+
 hipError_t launch_attend_join(int dtype, int d, const AttendArgs &a, int64_t queries,
                               hipStream_t stream) {
-  const dim3 grid((unsigned)queries), block(64 * AP_JOIN);
   if (dtype == DT_F32) {
-    if (d == 64) hipLaunchKernelGGL((attend_join_kernel<DT_F32, 64>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((attend_join_kernel<DT_F32, 128>), grid, block, 0, stream, a);
+    if (d == 64) attend_join_run<DT_F32, 64>(a, queries, stream);
+    else attend_join_run<DT_F32, 128>(a, queries, stream);
   } else if (dtype == DT_F16) {
-    if (d == 64) hipLaunchKernelGGL((attend_join_kernel<DT_F16, 64>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((attend_join_kernel<DT_F16, 128>), grid, block, 0, stream, a);
+    if (d == 64) attend_join_run<DT_F16, 64>(a, queries, stream);
+    else attend_join_run<DT_F16, 128>(a, queries, stream);
   } else {
-    if (d == 64) hipLaunchKernelGGL((attend_join_kernel<DT_BF16, 64>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((attend_join_kernel<DT_BF16, 128>), grid, block, 0, stream, a);
+    if (d == 64) attend_join_run<DT_BF16, 64>(a, queries, stream);
+    else attend_join_run<DT_BF16, 128>(a, queries, stream);
   }
   return hipGetLastError();
 }

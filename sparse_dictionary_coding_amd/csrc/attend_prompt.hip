@@ -536,7 +536,7 @@ static int prompt_columns(int dtype) { return dtype == DT_F32 ? 16 * PR_WAVES : 
 int attend_prompt_splits(int dtype, int64_t R, int64_t n, int32_t kv_heads, int32_t group,
                          int64_t visible) {
   const int64_t wgs = (n * group / prompt_columns(dtype) + (R < n ? R : n)) * kv_heads;
-  int64_t s = wgs > 0 ? (PM_FILL + wgs - 1) / wgs : 1;
+  int64_t s = wgs > 0 ? PM_FILL / wgs : 1;
   const int64_t least = dtype == DT_F32 ? PR_LEAST : PM_LEAST;
   const int64_t most = (visible + least - 1) / least;
   s = s < most ? s : most;
