@@ -294,7 +294,8 @@ typedef struct {
  *   status          device int32 [R]: FADKV_ROW_*
  *   slots, positions  device int32 [max_tokens]: every new token's slot (-1 in a refused row) and
  *                   its position in the row; both -1 behind the last new token (a padded batch)
- * The arrays are distinct except as said.  0 <= R <= 8192, num_pages * page_size < 2^31, 1 <=
+ * Every page belongs to one row at a time (pages that several rows read, as a common prefix, are the
+ * caller's to hand out and take back).  The arrays are distinct except as said.  0 <= R <= 8192, num_pages * page_size < 2^31, 1 <=
  * max_pages, max_pages * page_size + max_tokens < 2^31, R * max_pages < 2^31.
  * workspace: fadkv_pages_workspace_bytes(R), 4-byte aligned. */
 int fadkv_pages_workspace_bytes(int64_t R, size_t *bytes);
@@ -329,7 +330,7 @@ int fadkv_rope_freqs(int32_t rot_dim, double base, int32_t kind, double factor, 
 
 /* The heads of n tokens, as a projection leaves them. */
 typedef struct {
-  int64_t n;              /* tokens, padding included, 0 .. 2^24 */
+  int64_t n;              /* tokens, padding included, 0 .. 2^23 */
   int32_t heads;          /* query heads, 1 .. 16384 */
   int32_t kv_heads;       /* key and value heads, 1 .. 256 */
   int32_t d;              /* 64 or 128 */
@@ -370,8 +371,8 @@ int fadkv_norm_rope(const fadkv_qkv *in, void *q_out, const fadkv_pages *pages,
  *   q, out  device [R][heads][d] in pages->dtype, 16-byte aligned, distinct
  *   max_len an upper bound of lens that sizes the split over the length (any larger length is
  *           still right, only slower); 1 .. max_pages * page_size
- * heads a multiple of kv_heads, heads / kv_heads <= 64, R * heads <= 2^22, window >= 0,
- * sinks >= 0, scale finite.  Scores and sums are fp32; the weights p are rounded to dtype for the
+ * heads a multiple of kv_heads, heads / kv_heads <= 64, R * heads <= 2^22, max_pages * page_size
+ * <= 2^30, window >= 0, sinks >= 0, scale finite.  Scores and sums are fp32; the weights p are rounded to dtype for the
  * product with v.  Results do not depend on the run (no atomics).  workspace:
  * fadkv_attend_paged_workspace_bytes() bytes (0 where no split is needed), 256-byte aligned. */
 int fadkv_attend_paged_workspace_bytes(const fadkv_pages *pages, int64_t R, int32_t heads,

@@ -10,13 +10,14 @@
 namespace {
 
 constexpr int64_t kMaxRows = 8192;                  // the rows' prefix sums live in LDS
-constexpr int64_t kMaxTokens = int64_t(1) << 24;    // one workgroup per token
+constexpr int64_t kMaxTokens = int64_t(1) << 23;    // a workgroup of 256 per token: 2^31 work-items
 constexpr int64_t kMaxRowHeads = int64_t(1) << 22;  // the attention grids
 constexpr int64_t kMaxPromptHeads = int64_t(1) << 28;
 constexpr int kMaxKvHeads = 256;
 constexpr int kMaxGroup = 64;
 constexpr int kMaxHeads = kMaxKvHeads * kMaxGroup;
 constexpr int64_t kTwo31 = int64_t(1) << 31;
+constexpr int64_t kMaxRowTokens = int64_t(1) << 30;  // positions rounded up to tiles stay below 2^31
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -57,7 +58,7 @@ int check_heads(const fadkv_pages *p, int64_t R, int32_t heads) {
 // the tables both attention calls take
 int check_rows(const fadkv_pages *p, int32_t max_pages, float scale, int32_t window,
                int32_t sinks) {
-  if (max_pages < 1 || (int64_t)max_pages * p->page_size >= kTwo31) return FADKV_ERR_SHAPE;
+  if (max_pages < 1 || (int64_t)max_pages * p->page_size > kMaxRowTokens) return FADKV_ERR_SHAPE;
   if (!isfinite(scale) || window < 0 || sinks < 0) return FADKV_ERR_ARG;
   return FADKV_OK;
 }
@@ -269,7 +270,7 @@ int fadkv_attend_paged(const fadkv_pages *pages, const int32_t *table, int32_t m
     return FADKV_ERR_SHAPE;
   if (R == 0) return FADKV_OK;
   if (!table || !lens || !q || !out || !aligned(table, 4) || !aligned(lens, 4) ||
-      !aligned(q, 16) || !aligned(out, 16))
+      !aligned(q, 16) || !aligned(out, 16) || q == out)
     return FADKV_ERR_ARG;
   fadkv::AttendArgs a =
       attend_args(pages, table, max_pages, lens, R, q, heads, scale, window, sinks, out);
@@ -305,7 +306,7 @@ int fadkv_attend_prompt(const fadkv_pages *pages, const int32_t *table, int32_t 
     return FADKV_ERR_SHAPE;
   if (R == 0 || n == 0) return FADKV_OK;
   if (!table || !lens || !cu || !q || !out || !aligned(table, 4) || !aligned(lens, 4) ||
-      !aligned(cu, 4) || !aligned(q, 16) || !aligned(out, 16))
+      !aligned(cu, 4) || !aligned(q, 16) || !aligned(out, 16) || q == out)
     return FADKV_ERR_ARG;
   fadkv::AttendArgs a =
       attend_args(pages, table, max_pages, lens, R, q, heads, scale, window, sinks, out);

@@ -31,7 +31,7 @@ constexpr int AP_MANY = 4096;     // where there are more queries than this
 int attend_paged_splits(int64_t R, int32_t kv_heads, int32_t group, int64_t visible) {
   const int64_t wgs = R * kv_heads * ((group + 15) / 16);
   int64_t s = wgs > 0 ? (AP_FILL + wgs - 1) / wgs : 1;
-  if (R > 1 && s < AP_ROWS) s = AP_ROWS;
+  if (R > 1 && s < AP_ROWS && wgs < AP_FILL * 8) s = AP_ROWS;   // beyond that the ends even out
   const int64_t most = (visible + AP_LEAST - 1) / AP_LEAST;
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s);

@@ -258,6 +258,21 @@ __device__ __forceinline__ bool attend_tile(KvTile<DT, D, ONCE> &kv, const uint4
   return true;
 }
 
+// c + the products of 16 bytes of two rows
+template <int DT> __device__ __forceinline__ float dot16(const uint4 &a, const uint4 &b, float c) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == DT_F32) {
+      c = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), c);
+    } else {
+      c = fmaf(lo_f<DT>(x[i]), lo_f<DT>(y[i]), c);
+      c = fmaf(hi_f<DT>(x[i]), hi_f<DT>(y[i]), c);
+    }
+  }
+  return c;
+}
+
 // One column by itself over tiles [i0, i1) of `step` <= 64 tokens, a token per lane: nothing that the
 // column does not see is multiplied, whatever it holds.  The path of blocks that
 // hold an infinity or NaN where the tiles above cannot keep it from the columns that do not see it.
@@ -284,7 +299,10 @@ __device__ __forceinline__ void attend_column(const PageView &pv, const uint8_t 
     float z = -__builtin_inff();
     if (on) {
       float dot = 0.f;
-      for (int e = 0; e < D; ++e) dot = fmaf(elem_f<DT>(qrow, e), elem_f<DT>(pv.k + at, e), dot);
+      const uint4 *qv = reinterpret_cast<const uint4 *>(qrow);
+      const uint4 *kv = reinterpret_cast<const uint4 *>(pv.k + at);
+#pragma unroll 4
+      for (int c = 0; c < ROWB / 16; ++c) dot = dot16<DT>(qv[c], kv[c], dot);
       z = dot * scale2;
     }
     float top = z;

@@ -740,6 +740,7 @@ def fadkv_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions
     pos = _ptr(positions, "positions", _I32, (n,), dev)
     rot, fr = 0, None
     if freqs is not None:
+        _device_of(freqs, "freqs")
         rot = 2 * freqs.numel()
         fr = _ptr(freqs, "freqs", torch.float64, (rot // 2,), dev) if rot else None
     qw = None if q_weight is None else _ptr(q_weight, "q_weight", dt, (d,), dev)
@@ -777,6 +778,7 @@ def _attend_args(pages, table, lens, q, out, dev):
     """Checks what both attention calls take; returns (pages struct, addresses, out, shapes)."""
     p = pages.c()
     dt = pages.k.dtype
+    _device_of(table, "table")
     if q.dim() != 3 or table.dim() != 2:
         raise ValueError("q must be [..][heads][d] and table [R][max_pages]")
     n, heads = q.shape[0], q.shape[1]

@@ -20,6 +20,7 @@ pytestmark = pytest.mark.skipif(not os.path.exists(fadkv.LIB_PATH),
                                 reason="libfadkv.so not built (run __graft_entry__.build())")
 
 FAKE = 0x7F0000100000          # 256-byte aligned
+FAKE2 = 0x7F0000200000
 I31 = (1 << 31) - 1
 
 
@@ -148,7 +149,7 @@ def _norm_rope(q_out=FAKE, pages=None, slots=None, k_rows=None, v_rows=None, **k
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(dtype=3), -2), (dict(d=96), -3), (dict(n=-1), -3), (dict(n=(1 << 24) + 1), -3),
+    (dict(dtype=3), -2), (dict(d=96), -3), (dict(n=-1), -3), (dict(n=(1 << 23) + 1), -3),
     (dict(heads=0), -3), (dict(kv_heads=0), -3), (dict(kv_heads=257), -3), (dict(heads=16385), -3),
     (dict(rot_dim=72), -3), (dict(rot_dim=80), -3), (dict(rot_dim=-16), -3), (dict(interleaved=2), -1),
     (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(mscale=float("inf")), -1),
@@ -181,17 +182,17 @@ BAD_ATTEND = [(dict(heads=12), -3), (dict(heads=0), -3), (dict(heads=8 * 65), -3
               (dict(scale=float("nan")), -1), (dict(window=-1), -1), (dict(sinks=-2), -1),
               (dict(table=None), -1), (dict(lens=None), -1), (dict(q=None), -1), (dict(out=None), -1),
               (dict(table=FAKE + 2), -1), (dict(lens=FAKE + 1), -1), (dict(q=FAKE + 8), -1),
-              (dict(out=FAKE + 4), -1)]
+              (dict(out=FAKE + 4), -1), (dict(out=FAKE2), -1), (dict(max_pages=(1 << 26) + 1), -3)]
 
 
-def _paged(pages=None, table=FAKE, max_pages=8, lens=FAKE, R=4, q=FAKE, heads=32, scale=0.1,
+def _paged(pages=None, table=FAKE, max_pages=8, lens=FAKE, R=4, q=FAKE2, heads=32, scale=0.1,
            window=0, sinks=0, max_len=100, out=FAKE, ws=FAKE, ws_bytes=1 << 40):
     return fadkv.lib().fadkv_attend_paged(ctypes.byref(pages or _pages()), table, max_pages, lens,
                                           R, q, heads, scale, window, sinks, max_len, out, ws,
                                           ws_bytes, None)
 
 
-def _prompt(pages=None, table=FAKE, max_pages=8, lens=FAKE, cu=FAKE, R=4, q=FAKE, n=20, heads=32,
+def _prompt(pages=None, table=FAKE, max_pages=8, lens=FAKE, cu=FAKE, R=4, q=FAKE2, n=20, heads=32,
             scale=0.1, window=0, sinks=0, max_len=100, out=FAKE, ws=FAKE, ws_bytes=1 << 40):
     return fadkv.lib().fadkv_attend_prompt(ctypes.byref(pages or _pages()), table, max_pages, lens,
                                            cu, R, q, n, heads, scale, window, sinks, max_len, out,

@@ -682,6 +682,30 @@ def test_two_graphs_share_a_workspace_and_streams_do_not_mix():
     assert all(torch.equal(a, b) for a, b in zip(ref, got))
 
 
+def test_raw_and_null_stream_handles():
+    _banner("stream handles")
+    pages, table = _cache("f16", 1, 64, 16, [300])
+    q = torch.randn(1, 2, 64, device=DEV).half()
+    ref = fadkv.fadkv_attend_paged(pages, table, _i32([300]), q, 0.1)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for handle in (0, s, s.cuda_stream, torch.cuda.default_stream()):
+        L = _i32([300])
+        torch.cuda.synchronize()
+        got = fadkv.fadkv_attend_paged(pages, table, L, q, 0.1, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(ref, got)
+
+
+def test_attend_prompt_full_of_nan_ends():
+    """Every value a NaN: the slow path of every block, at a size where its time shows."""
+    _banner("prompt full of NaN")
+    pages, table = _cache("bf16", 1, 128, 64, [1500])
+    pages.v.fill_(float("nan"))
+    q = torch.randn(1500, 4, 128, device=DEV).bfloat16()
+    assert fadkv.fadkv_attend_prompt(pages, table, _i32([1500]), _i32([0, 1500]), q, 0.1).isnan().all()
+
+
 def test_binding_refusals():
     _banner("binding refusals")
     pages, table = _cache("f16", 1, 64, 16, [20])
