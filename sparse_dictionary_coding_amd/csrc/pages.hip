@@ -7,10 +7,13 @@
 // can be filled in any order.
 //
 // What bounds it: latency.  A step moves a few KB, so the time is the launches and the chain
-// length -> sums -> ring entry -> table and slot.  Small batches run as ONE workgroup that keeps
-// the sums and row records in LDS and fills everything itself; larger ones scan with one
-// workgroup and fill with many (tokens by a binary search of their row in an LDS copy of cu,
-// pages with one wave per row).
+// length -> sums -> ring entry -> table and slot.  Up to 1024 rows the sums and row records fit
+// LDS: a small step is ONE workgroup that scans and fills everything itself (64 rows of one token:
+// 3.6 us), and a large one is many that each scan all rows and fill a part, as long as none of
+// them can see the new lengths that the first one stores (lens_out and ring_state_out are
+// arrays of their own).  Otherwise one workgroup scans and many fill: tokens by a binary search of
+// their row in an LDS copy of cu, pages with one wave per row (256 rows, 262144 tokens: 11.6 us for
+// the two launches).
 #include "common.h"
 #include "dense.h"
 
@@ -24,6 +27,7 @@ constexpr int FILL_TOKENS = 4 * FILL_THREADS;   // tokens per fill workgroup
 constexpr int MAX_ROWS = 8192;                  // rows of one call: their cu fits LDS (32 KB)
 constexpr int ONE_ROWS = SCAN_THREADS;          // one-workgroup form: a row per thread,
 constexpr int ONE_TOKENS = 4 * SCAN_THREADS;    // and a few tokens per thread
+constexpr int MAX_GRID = 1024;                  // workgroups that scan for themselves
 
 // prefix sums over rows; need and back stay below R * max_pages < 2^31
 struct Sums {
@@ -125,9 +129,10 @@ __global__ __launch_bounds__(SCAN_THREADS) void pages_scan_kernel(PagesArgs a) {
   int head = a.ring_state[0], count = a.ring_state[1];
   head = head < 0 || head >= a.num_pages ? 0 : head;
   count = count < 0 ? 0 : (count > a.num_pages ? a.num_pages : count);
+  const bool first = blockIdx.x == 0;   // stores what there is one of
   if (tid == 0) {
     s_taken = 0;
-    a.cu[0] = 0;
+    if (first) a.cu[0] = 0;
     if constexpr (ONE) s_cu[0] = 0;
   }
   Sums carry = {0, 0, 0};
@@ -159,10 +164,12 @@ __global__ __launch_bounds__(SCAN_THREADS) void pages_scan_kernel(PagesArgs a) {
                        : (ok && need > 0 ? wrapped(head + (int)s.need - need, a.num_pages) : 0);
       row.ok = ok;
       if (ok && need > 0) atomicMax(&s_taken, (int)s.need);
-      a.lens_out[r] = gone ? 0 : (ok ? (int)(len + add) : len);
-      a.status[r] = gone ? FADKV_ROW_RELEASED : (ok ? FADKV_ROW_OK : FADKV_ROW_REFUSED);
       const int end = (int)(s.add < a.max_tokens ? s.add : a.max_tokens);
-      a.cu[r + 1] = end;
+      if (first) {
+        a.lens_out[r] = gone ? 0 : (ok ? (int)(len + add) : len);
+        a.status[r] = gone ? FADKV_ROW_RELEASED : (ok ? FADKV_ROW_OK : FADKV_ROW_REFUSED);
+        a.cu[r + 1] = end;
+      }
       if constexpr (ONE) {
         s_cu[r + 1] = end;
         s_row[r] = row;
@@ -172,17 +179,24 @@ __global__ __launch_bounds__(SCAN_THREADS) void pages_scan_kernel(PagesArgs a) {
     }
   }
   __syncthreads();
-  if (tid == 0) {
+  if (first && tid == 0) {
     const int taken = s_taken;
     a.ring_state_out[0] = wrapped(head + taken, a.num_pages);
     const long long left = (long long)count - taken + carry.back;
     a.ring_state_out[1] = (int)(left > a.num_pages ? a.num_pages : left);
   }
   if constexpr (ONE) {
-    for (int j = tid; j < a.max_tokens; j += (int)blockDim.x) {
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t j = (int64_t)blockIdx.x * blockDim.x + tid; j < a.max_tokens; j += step) {
       const bool in = j < s_cu[a.R];
-      const int r = in ? row_of(s_cu, a.R, j) : 0;
-      fill_token(a, j, r, in, s_cu[r], s_row[r]);
+      const int r = in ? row_of(s_cu, a.R, (int)j) : 0;
+      fill_token(a, (int)j, r, in, s_cu[r], s_row[r]);
+    }
+    if (gridDim.x > 1) {   // a wave per row
+      const int waves = (int)(gridDim.x * (blockDim.x >> 6));
+      for (int r = (int)(blockIdx.x * (blockDim.x >> 6)) + (tid >> 6); r < a.R; r += waves)
+        fill_pages(a, r, s_row[r], tid & 63, 64);
+      return;
     }
     // a thread moves its row's few pages, a wave those of each row with many
     constexpr int FEW = 4;
@@ -225,10 +239,17 @@ __global__ __launch_bounds__(FILL_THREADS) void pages_fill_kernel(PagesArgs a, i
 }
 
 hipError_t launch_pages_advance(const PagesArgs &a, hipStream_t stream) {
-  if (a.R <= ONE_ROWS && a.max_tokens <= ONE_TOKENS) {
-    const int most = a.R > a.max_tokens ? a.R : a.max_tokens;
-    const int threads = most <= 64 ? 64 : (most <= 256 ? 256 : SCAN_THREADS);
-    hipLaunchKernelGGL(pages_scan_kernel<true>, dim3(1), dim3(threads), 0, stream, a);
+  const bool apart = a.lens_out != a.lens && a.ring_state_out != a.ring_state;
+  if (a.R <= ONE_ROWS && (a.max_tokens <= ONE_TOKENS || apart)) {
+    const int64_t most = a.R > a.max_tokens ? a.R : a.max_tokens;
+    int threads = most <= 64 ? 64 : (most <= 256 ? 256 : SCAN_THREADS);
+    int64_t grid = 1;
+    if (a.max_tokens > ONE_TOKENS) {
+      threads = a.R <= FILL_THREADS ? FILL_THREADS : SCAN_THREADS;
+      grid = (a.max_tokens + (int64_t)4 * threads - 1) / (4 * threads);   // four tokens a thread,
+      if (grid > MAX_GRID) grid = MAX_GRID;                                // until the chip is full
+    }
+    hipLaunchKernelGGL(pages_scan_kernel<true>, dim3((unsigned)grid), dim3(threads), 0, stream, a);
     return hipGetLastError();
   }
   const int threads = a.R <= 64 ? 64 : (a.R <= 256 ? 256 : SCAN_THREADS);

@@ -40,15 +40,18 @@ def _banner(msg):
 
 
 # ---- bookkeeping --------------------------------------------------------------------------------
-def _advance_both(page, new, lens, table, ring, state, tokens, **kw):
+def _advance_both(page, new, lens, table, ring, state, tokens):
+    """Into arrays of their own and in place, which large steps run by other kernels."""
     ref = dense_oracle.pages_advance(page, new, lens, table, ring, state, tokens)
-    pt = fadkv.PageTable(_i32(table), _i32(lens), _i32(ring), _i32(state), page)
-    step = fadkv.fadkv_pages_advance(pt, _i32(new), tokens, **kw)
-    torch.cuda.synchronize()
-    got = {"table": pt.table, "ring": pt.ring, "lens": step.lens, "ring_state": step.ring_state,
-           "cu": step.cu, "status": step.status, "slots": step.slots, "positions": step.positions}
-    for name, t in got.items():
-        np.testing.assert_array_equal(t.cpu().numpy(), ref[name], err_msg=name)
+    for in_place in (False, True):
+        pt = fadkv.PageTable(_i32(table), _i32(lens), _i32(ring), _i32(state), page)
+        step = fadkv.PageStep.empty(pt, tokens, in_place=in_place)
+        fadkv.fadkv_pages_advance(pt, _i32(new), out=step)
+        torch.cuda.synchronize()
+        got = {"table": pt.table, "ring": pt.ring, "lens": step.lens, "ring_state": step.ring_state,
+               "cu": step.cu, "status": step.status, "slots": step.slots, "positions": step.positions}
+        for name, t in got.items():
+            np.testing.assert_array_equal(t.cpu().numpy(), ref[name], err_msg=f"{name} {in_place}")
     return ref
 
 
