@@ -241,6 +241,8 @@ __device__ __forceinline__ bool attend_tile(KvTile<DT, D, ONCE> &kv, const uint4
       for (int e = 0; e < T::EP; ++e)
         st.o[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kv.v[j][e]), p[j], st.o[e], 0, 0, 0);
   } else {
+    // p to the type of v: the matrix cores take no other, and half a step of it (2^-9 in bf16, random
+    // over the tokens) is what the output's own rounding costs; the sum above is of p itself
     const uint4 pb = make_uint4(round2<DT>(p[0], p[1]), round2<DT>(p[2], p[3]),
                                 round2<DT>(p[4], p[5]), round2<DT>(p[6], p[7]));
 #pragma unroll

@@ -4,7 +4,8 @@
 //   t = position * f_i, (a, b) = elements (2i, 2i+1) or (i, i + rot/2) of the head.
 //
 // What bounds it: HBM.  Every value is read once and written once (keys and values twice where the
-// encoder's rows are wanted); a token's other data is 8 bytes.  So a head is one 16-byte (two in
+// encoder's rows are wanted); a token's other data is 8 bytes.  16384 tokens of 32 + 2 * 8 heads of 128
+// in bf16 with rows: 470 MB in 79 to 85 us, 5.5 to 6.0 TB/s; 16 tokens: 5 us of latency.  So a head is one 16-byte (two in
 // fp32) load per lane, d / 8 lanes a head, a wave's loads contiguous, and everything between load
 // and store stays in registers: the sum of squares by DPP within the lanes of the head, the
 // partner elements of the half layout by a lane exchange of the packed input.
