@@ -254,7 +254,9 @@ int fadkv_attend_paged_workspace_bytes(const fadkv_pages *pages, int64_t R, int3
   FADKV_TRY(check_heads(pages, R, heads));
   if (max_len < 1) return FADKV_ERR_SHAPE;
   *bytes = attend_part_bytes(
-      R * heads, fadkv::attend_paged_splits(R, pages->kv_heads, heads / pages->kv_heads, max_len),
+      R * heads,
+      fadkv::attend_paged_most_splits(pages->dtype, R, pages->kv_heads, heads / pages->kv_heads,
+                                      max_len),
       pages->d);
   return FADKV_OK;
 }
@@ -274,10 +276,12 @@ int fadkv_attend_paged(const fadkv_pages *pages, const int32_t *table, int32_t m
     return FADKV_ERR_ARG;
   fadkv::AttendArgs a =
       attend_args(pages, table, max_pages, lens, R, q, heads, scale, window, sinks, out);
-  a.splits = fadkv::attend_paged_splits(R, a.kv_heads, a.group,
-                                        visible_bound(max_len, window, sinks));
+  const int64_t visible = visible_bound(max_len, window, sinks);
+  a.splits = fadkv::attend_paged_splits(pages->dtype, R, a.kv_heads, a.group, visible);
   FADKV_TRY(take_parts(a, R * heads, pages->d, workspace, workspace_bytes));
-  return fadkv::launch_attend_paged(pages->dtype, pages->d, a, stream) == hipSuccess
+  return fadkv::launch_attend_paged(pages->dtype, pages->d, a,
+                                    fadkv::attend_paged_waves(pages->dtype, visible),
+                                    stream) == hipSuccess
              ? FADKV_OK : FADKV_ERR_HIP;
 }
 

@@ -4,20 +4,27 @@
 // running maximum and sum.  What bounds it: HBM.  Every visible key and value is read once, by
 // one wave, for all query heads of its kv head (up to 16 columns of the matrix instruction), at
 // 4 d heads / (4 d kv_heads) = one to a few flops a byte.  8 kv heads of 128 in 16 bits: one row of
-// 262144 tokens 6.3 to 6.5 TB/s, 64 of 4096 6.2, where a bare read stream reaches 7.2 (6.1 with the
-// 64-byte pieces of rows that a matrix operand of keys asks for).
+// 262144 tokens and 64 of 4096 6.1 to 6.4 TB/s, where a bare read stream reaches 7.2.
+//
+// Keys are read in whole rows like values: the 64-byte pieces of 16 rows that a matrix operand of keys
+// asks for reach 6.1 TB/s in a bare read where whole rows reach 7.0.  A wave holds one tile, and what
+// hides the loads is the other waves, three a SIMD (two tiles a wave, loaded in pieces: 64 ragged
+// rows 108 us against 99, a window of 1024 18.7 against 17.3, 64 rows of 4096 tokens 171 against 175).
 //
 // A row's 32-token tiles are split over up to `splits` workgroups, each an equal share of the row's
-// own length, and dealt to a workgroup's four waves in turn.  The waves' (maximum, sum, output) are joined in LDS, the
-// workgroups' through the workspace by a second kernel.
+// own length, and dealt to a workgroup's waves in turn.  The waves' (maximum, sum, output) are joined
+// in LDS, the workgroups' through the workspace by a second kernel.
 #include "attend_tile.h"
 
 namespace fadkv {
 
 namespace {
 
-constexpr int AP_WAVES = 4;
-constexpr int AP_FILL = 512;      // workgroups that are resident at once: two on each of the 256 CUs
+// Waves of a workgroup: eight where queries see many tokens, four where they see few and a wave of
+// eight would have none or one of the tiles (64 ragged rows to 4096 tokens: 99 us with eight, 101 with
+// four; one row of 131072: 91 and 92; a window of 1024: 19.3 and 17.3).
+constexpr int AP_SHORT = 2048;
+constexpr int AP_FILL = 2048;     // waves in all: two on each SIMD of the 256 CUs
 constexpr int AP_ROWS = 4;        // splits of a row of several
 constexpr int AP_LEAST = 256;     // tokens below which a share is not cut further
 constexpr int AP_JOIN = 4;        // waves that join a query's splits
@@ -26,17 +33,28 @@ constexpr int AP_MANY = 4096;     // where there are more queries than this
 
 }  // namespace
 
-// As many splits as fill the chip in one round (measured at one row of 131072 tokens, 8 kv heads of
-// 128 in bf16: 512 workgroups 92 us, 1024 99, 2048 111), but four where there are several rows, so
-// that the end does not wait for the longest row (64 rows of 1 to 4096 tokens in fp16: four splits
-// 108 us, one 123).
-int attend_paged_splits(int64_t R, int32_t kv_heads, int32_t group, int64_t visible) {
+int attend_paged_waves(int dtype, int64_t visible) {
+  return dtype == DT_F32 || visible <= AP_SHORT ? 4 : 8;
+}
+
+// As many splits as fill the chip in one round (one row of 131072 tokens: 92 us, 99 in two rounds, 111
+// in four), but four where there are several rows, so that the end does not wait for the longest
+// (64 rows of 1 to 4096 tokens: four splits 108 us, one 123).
+int attend_paged_splits(int dtype, int64_t R, int32_t kv_heads, int32_t group, int64_t visible) {
   const int64_t wgs = R * kv_heads * ((group + 15) / 16);
-  int64_t s = wgs > 0 ? (AP_FILL + wgs - 1) / wgs : 1;
-  if (R > 1 && s < AP_ROWS && wgs < AP_FILL * 8) s = AP_ROWS;   // beyond that the ends even out
+  const int64_t fill = AP_FILL / attend_paged_waves(dtype, visible);
+  int64_t s = wgs > 0 ? (fill + wgs - 1) / wgs : 1;
+  if (R > 1 && s < AP_ROWS && wgs < fill * 8) s = AP_ROWS;   // beyond that the ends even out
   const int64_t most = (visible + AP_LEAST - 1) / AP_LEAST;
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s);
+}
+
+// A window may leave few visible tokens of a long cache, which asks for more splits.
+int attend_paged_most_splits(int dtype, int64_t R, int32_t kv_heads, int32_t group, int64_t len) {
+  const int far = attend_paged_splits(dtype, R, kv_heads, group, len);
+  const int near = attend_paged_splits(dtype, R, kv_heads, group, len < AP_SHORT ? len : AP_SHORT);
+  return far > near ? far : near;
 }
 
 // the visible tiles of a row: those of the first tokens, then those of the window
@@ -66,10 +84,13 @@ __device__ __forceinline__ int share_of(int count, int splits) {
   return share < AP_LEAST / 32 ? AP_LEAST / 32 : share;
 }
 
-template <int DT, int D, bool SPLIT>
-__global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendArgs a) {
+template <int DT, int D, int AP_WAVES, bool SPLIT>
+__global__ __launch_bounds__(64 * AP_WAVES, DT == DT_F32 ? 2 : 3) void attend_paged_kernel(AttendArgs a) {
   using T = AttTile<DT, D>;
+  using Tile = KvTile<DT, D, true, DT != DT_F32>;
+  // a wave's own: its keys on their way to operands, then its output to be joined
   __shared__ __attribute__((aligned(16))) float s_o[AP_WAVES][16][D + 4];
+  static_assert(DT == DT_F32 || 32 * T::ROWB <= sizeof(s_o[0]), "32 rows fit");
   __shared__ float s_m[AP_WAVES][16], s_l[AP_WAVES][16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -111,12 +132,12 @@ __global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendAr
   const float scale2 = a.scale * kLog2e;
 
   // Pages of the wave's tiles: lane k holds those of its k-th tile from here, so that a tile's
-  // loads wait for no table entry; and a tile is loaded while the one before it is worked on.
+  // loads wait for no table entry.
   //
   // Every row and split starts at another of its tiles and comes round: rows whose pages follow one
   // another in the pool lie a power of two apart, and workgroups that walk them in step would
   // meet on the same memory channels (64 rows of 4096 tokens in pages of 16, in order: 173 us
-  // against 223 us; pages in random order: 172 and 171).
+  // against 223 us).
   const int mine = i1 > i0 ? i1 - i0 : 1;
   const int turn = (11 * r + 5 * split) % mine;
   const auto start_of = [&](int i) {
@@ -124,7 +145,7 @@ __global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendAr
     return (i < tl.first ? i : tl.from + i - tl.first) << 5;
   };
   int ids0 = -1, ids1 = -1;
-  const auto fetch = [&](KvTile<DT, D, true> &kv, int i) {
+  const auto fetch = [&](Tile &kv, int i) {
     const int k = (i - i0) / AP_WAVES;   // the wave's tile number
     if ((k & 63) == 0) {
       const int at = i + lane * AP_WAVES;
@@ -136,31 +157,18 @@ __global__ __launch_bounds__(64 * AP_WAVES, 2) void attend_paged_kernel(AttendAr
   };
   AttState<DT, D> st;
   st.clear();
-  const auto attend = [&](KvTile<DT, D, true> &kv, int i) {
+  const auto attend = [&](Tile &kv, int i) {
+    if constexpr (DT != DT_F32) kv.turn(reinterpret_cast<uint8_t *>(&s_o[wave][0][0]), lane);
     const int t0 = start_of(i);
     const bool whole = kv.there[0] && kv.there[1] && t0 + 32 <= see.hi &&
                        (t0 >= see.lo || t0 + 32 <= a.sinks);
     attend_tile<DT, D, false>(kv, q, t0, whole, see, see, a.sinks, scale2, lane, st);
   };
   int i = i0 + wave;
-  if constexpr (DT == DT_F32) {   // two tiles of fp32 do not fit the registers of two waves a SIMD
-    KvTile<DT, D, true> kv;
-    for (; i < i1; i += AP_WAVES) {
-      fetch(kv, i);
-      attend(kv, i);
-    }
-  } else {
-    KvTile<DT, D, true> even, odd;
-    if (i < i1) fetch(even, i);
-    while (i < i1) {
-      if (i + AP_WAVES < i1) fetch(odd, i + AP_WAVES);
-      attend(even, i);
-      i += AP_WAVES;
-      if (i >= i1) break;
-      if (i + AP_WAVES < i1) fetch(even, i + AP_WAVES);
-      attend(odd, i);
-      i += AP_WAVES;
-    }
+  Tile kv;
+  for (; i < i1; i += AP_WAVES) {
+    fetch(kv, i);
+    attend(kv, i);
   }
 
   // join the waves
@@ -330,24 +338,35 @@ hipError_t launch_attend_join(int dtype, int d, const AttendArgs &a, int64_t que
   return hipGetLastError();
 }
 
-template <int DT, int D>
+template <int DT, int D, int WAVES>
 static hipError_t attend_paged_run(const AttendArgs &a, hipStream_t stream) {
   const unsigned wgs = (unsigned)((size_t)a.R * a.kv_heads * ((a.group + 15) / 16));
+  const dim3 block(64 * WAVES);
   if (a.splits > 1) {
-    hipLaunchKernelGGL((attend_paged_kernel<DT, D, true>), dim3(wgs * a.splits),
-                       dim3(64 * AP_WAVES), 0, stream, a);
+    hipLaunchKernelGGL((attend_paged_kernel<DT, D, WAVES, true>), dim3(wgs * a.splits), block, 0, stream, a);
     return launch_attend_join(DT, D, a, (int64_t)a.R * a.kv_heads * a.group, stream);
   }
-  hipLaunchKernelGGL((attend_paged_kernel<DT, D, false>), dim3(wgs), dim3(64 * AP_WAVES), 0, stream, a);
+  hipLaunchKernelGGL((attend_paged_kernel<DT, D, WAVES, false>), dim3(wgs), block, 0, stream, a);
   return hipGetLastError();
 }
 
-hipError_t launch_attend_paged(int dtype, int d, const AttendArgs &a, hipStream_t stream) {
+template <int DT, int D>
+static hipError_t attend_paged_run(const AttendArgs &a, int waves, hipStream_t stream) {
+  if constexpr (DT != DT_F32)
+    if (waves == 8) return attend_paged_run<DT, D, 8>(a, stream);
+  return attend_paged_run<DT, D, 4>(a, stream);
+}
+
+hipError_t launch_attend_paged(int dtype, int d, const AttendArgs &a, int waves,
+                               hipStream_t stream) {
   if (dtype == DT_F32)
-    return d == 64 ? attend_paged_run<DT_F32, 64>(a, stream) : attend_paged_run<DT_F32, 128>(a, stream);
+    return d == 64 ? attend_paged_run<DT_F32, 64>(a, waves, stream)
+                   : attend_paged_run<DT_F32, 128>(a, waves, stream);
   if (dtype == DT_F16)
-    return d == 64 ? attend_paged_run<DT_F16, 64>(a, stream) : attend_paged_run<DT_F16, 128>(a, stream);
-  return d == 64 ? attend_paged_run<DT_BF16, 64>(a, stream) : attend_paged_run<DT_BF16, 128>(a, stream);
+    return d == 64 ? attend_paged_run<DT_F16, 64>(a, waves, stream)
+                   : attend_paged_run<DT_F16, 128>(a, waves, stream);
+  return d == 64 ? attend_paged_run<DT_BF16, 64>(a, waves, stream)
+                 : attend_paged_run<DT_BF16, 128>(a, waves, stream);
 }
 
 }  // namespace fadkv

@@ -149,7 +149,7 @@ __global__ __launch_bounds__(64 * PR_WAVES) void attend_prompt_kernel(AttendArgs
   bool fine = true;
   for (int i = i0; i < i1 && fine; ++i) {
     const int t0 = start_of(i);
-    KvTile<DT, D, false> kv;
+    KvTile<DT, D, false, false> kv;
     kv.load(pv, __builtin_amdgcn_readfirstlane(page_of(pv, t0)),
             __builtin_amdgcn_readfirstlane(page_of(pv, t0 + 16)), t0, lane);
     const bool whole = kv.there[0] && kv.there[1] && t0 + 32 <= all.hi &&

@@ -115,8 +115,10 @@ template <bool ONCE, class T> __device__ __forceinline__ T load_vec(const void *
   else return *static_cast<const T *>(p);
 }
 
-// keys and values of 32 tokens in registers
-template <int DT, int D, bool ONCE> struct KvTile {
+// Keys and values of 32 tokens in registers.  A matrix operand wants 16 bytes of each of 16 keys per
+// load; ROWS loads whole rows instead (1 KB of neighbouring bytes), which turn() then exchanges into
+// operands through LDS.
+template <int DT, int D, bool ONCE, bool ROWS> struct KvTile {
   uint4 k[2][AttTile<DT, D>::CH];
   uint32_t v[8][AttTile<DT, D>::VW];
   bool there[2];
@@ -131,10 +133,11 @@ template <int DT, int D, bool ONCE> struct KvTile {
       const int64_t at = group_at<T::ROWB>(pv, a ? id1 : id0, t0 + 16 * a);
       there[a] = at >= 0;
       if (there[a]) {
-        const u32x4_t *src = reinterpret_cast<const u32x4_t *>(pv.k + at + (size_t)r * T::ROWB);
+        const u32x4_t *src = reinterpret_cast<const u32x4_t *>(pv.k + at);
 #pragma unroll
         for (int i = 0; i < T::CH; ++i)
-          k[a][i] = __builtin_bit_cast(uint4, load_vec<ONCE, u32x4_t>(src + 4 * i + g));
+          k[a][i] = __builtin_bit_cast(uint4, load_vec<ONCE, u32x4_t>(
+              src + (ROWS ? 64 * i + lane : r * (T::ROWB / 16) + 4 * i + g)));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t *row =
@@ -162,6 +165,29 @@ template <int DT, int D, bool ONCE> struct KvTile {
       }
     }
   }
+
+  // ROWS: the keys into operand order, through 32 rows of the wave's own LDS.  Chunk c of row r lies
+  // at c ^ f(r), so that 16 rows' reads of one chunk hit distinct banks.
+  __device__ __forceinline__ void turn(uint8_t *lds, int lane) {
+    using T = AttTile<DT, D>;
+    constexpr int CPR = T::ROWB / 16;
+    const auto place = [](int row, int c) {
+      return (row * CPR + (c ^ (CPR == 16 ? row & 15 : (row >> 1) & 7))) * 16;
+    };
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int i = 0; i < T::CH; ++i) {
+        const int at = 64 * i + lane;
+        *reinterpret_cast<uint4 *>(lds + place(16 * a + at / CPR, at % CPR)) = k[a][i];
+      }
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int i = 0; i < T::CH; ++i)
+        k[a][i] = *reinterpret_cast<const uint4 *>(
+            lds + place(16 * a + (lane & 15), 4 * i + (lane >> 4)));
+  }
 };
 
 // Not 0 where a value of the 32-bit word (two in the 16-bit types) is an infinity or NaN: one added
@@ -176,8 +202,8 @@ template <int DT> __device__ __forceinline__ uint32_t odd_value(uint32_t w) {
 // Tokens that no column sees are zeroed in v: p = 0 does not undo an infinity or NaN there.  Where
 // the columns see different tokens (MIXED) the same holds for a token that some of them see: then
 // nothing is done and the answer is false (attend_column does such blocks).
-template <int DT, int D, bool MIXED, bool ONCE>
-__device__ __forceinline__ bool attend_tile(KvTile<DT, D, ONCE> &kv, const uint4 (&q)[AttTile<DT, D>::CH],
+template <int DT, int D, bool MIXED, bool ONCE, bool ROWS>
+__device__ __forceinline__ bool attend_tile(KvTile<DT, D, ONCE, ROWS> &kv, const uint4 (&q)[AttTile<DT, D>::CH],
                                             int t0, bool whole, const Visible &col,
                                             const Visible &any, int sinks, float scale2, int lane,
                                             AttState<DT, D> &st) {

@@ -51,10 +51,14 @@ struct AttendArgs {
 };
 // parts that a row's (attend_paged) or a block of columns' (attend_prompt) tokens are split into, at
 // most; `visible` bounds the tokens that one query sees
-int attend_paged_splits(int64_t R, int32_t kv_heads, int32_t group, int64_t visible);
+int attend_paged_splits(int dtype, int64_t R, int32_t kv_heads, int32_t group, int64_t visible);
+// the largest of it over all windows of a cache of `len` tokens
+int attend_paged_most_splits(int dtype, int64_t R, int32_t kv_heads, int32_t group, int64_t len);
+int attend_paged_waves(int dtype, int64_t visible);   // per workgroup
 int attend_prompt_splits(int dtype, int64_t R, int64_t n, int32_t kv_heads, int32_t group,
                          int64_t visible);
-hipError_t launch_attend_paged(int dtype, int d, const AttendArgs &a, hipStream_t stream);
+hipError_t launch_attend_paged(int dtype, int d, const AttendArgs &a, int waves,
+                               hipStream_t stream);
 hipError_t launch_attend_prompt(int dtype, int d, const AttendArgs &a, hipStream_t stream);
 // joins the parts of `queries` queries (token times heads plus head) to the output
 hipError_t launch_attend_join(int dtype, int d, const AttendArgs &a, int64_t queries,

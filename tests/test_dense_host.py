@@ -221,7 +221,15 @@ def test_attend_paged_refusals_of_its_own():
     assert f(ctypes.byref(_pages()), 1, 32, 0, ctypes.byref(out)) == -3
     assert f(ctypes.byref(_pages()), 1, 31, 10, ctypes.byref(out)) == -3
     assert f(ctypes.byref(_pages()), 1, 32, 10, None) == -1
-    # a window never needs more than the length it cuts
+    # no window needs more than the bytes for its cache: what it sees is at most that, and the bytes for
+    # a shorter cache are no more
+    for R, kv, group, dtype in ((1, 8, 4, 1), (1, 100, 1, 2), (2, 1, 17, 1), (70, 1, 1, 2), (3, 5, 2, 0)):
+        p, last = _pages(num_pages=1 << 14, kv_heads=kv, dtype=dtype), 0
+        for max_len in (1, 200, 300, 600, 1100, 2000, 2048, 2049, 2100, 4000, 5000, 70000, 131072):
+            assert f(ctypes.byref(p), R, kv * group, max_len, ctypes.byref(out)) == 0
+            assert out.value >= last
+            last = out.value
+    # a short cache needs none
     assert f(ctypes.byref(_pages()), 1, 32, 16, ctypes.byref(out)) == 0 and out.value == 0
 
 

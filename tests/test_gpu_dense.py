@@ -337,6 +337,8 @@ PAGED = [
     ("f32", 3, 1, 128, 32, [700, 65], 1, 1),
     ("bf16", 1, 8, 64, 16, [400, 80], 16, 100),                  # more first tokens than a tile
     ("f16", 1, 1, 128, 16, [3000], 100, 40),
+    ("f16", 2, 2, 64, 32, [2500, 2049, 31], 0, 0),               # eight waves a workgroup
+    ("bf16", 1, 16, 128, 16, [4500], 3000, 9),
 ]
 
 
