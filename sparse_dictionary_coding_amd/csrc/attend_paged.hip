@@ -25,7 +25,8 @@ namespace {
 // four; one row of 131072: 91 and 92; a window of 1024: 19.3 and 17.3).
 constexpr int AP_SHORT = 2048;
 constexpr int AP_FILL = 2048;     // waves in all: two on each SIMD of the 256 CUs
-constexpr int AP_ROWS = 4;        // splits of a row of several
+constexpr int AP_ROWS = 8;        // splits of a row of several, at most, beyond those that fill the chip
+constexpr int AP_LONG = 2048;     // tokens of such a split, half as many before the chip is full
 constexpr int AP_LEAST = 256;     // tokens below which a share is not cut further
 constexpr int AP_JOIN = 4;        // waves that join a query's splits
 constexpr int AP_FEW = 8;         // splits that one thread joins,
@@ -37,14 +38,20 @@ int attend_paged_waves(int dtype, int64_t visible) {
   return dtype == DT_F32 || visible <= AP_SHORT ? 4 : 8;
 }
 
-// As many splits as fill the chip in one round (one row of 131072 tokens: 92 us, 99 in two rounds, 111
-// in four), but four where there are several rows, so that the end does not wait for the longest
-// (64 rows of 1 to 4096 tokens: four splits 108 us, one 123).
+// As many splits as fill the chip in one round (one row of 131072 tokens: 88 us, 92 in two rounds, 100
+// in four).  Several rows are cut further, so that the end does not wait for the longest, where a
+// share is long enough to pay for its start and for the join (ragged rows, 1 / 2 / 4 / 8 splits:
+// 128 to 1024 tokens 53 / 59 / 64 / 64 us, 48 to 4096 93 / 85 / 84 / 94, 90 to 16384 320 / 291 / 281 / 289,
+// 16 to 16384 with two, four and eight 112 / 97 / 91).
 int attend_paged_splits(int dtype, int64_t R, int32_t kv_heads, int32_t group, int64_t visible) {
   const int64_t wgs = R * kv_heads * ((group + 15) / 16);
   const int64_t fill = AP_FILL / attend_paged_waves(dtype, visible);
   int64_t s = wgs > 0 ? (fill + wgs - 1) / wgs : 1;
-  if (R > 1 && s < AP_ROWS && wgs < fill * 8) s = AP_ROWS;   // beyond that the ends even out
+  if (R > 1 && wgs < fill * 8) {   // beyond that the ends even out
+    int64_t cut = visible / (wgs < fill ? AP_LONG / 2 : AP_LONG);
+    cut = cut < AP_ROWS ? cut : AP_ROWS;
+    s = s > cut ? s : cut;
+  }
   const int64_t most = (visible + AP_LEAST - 1) / AP_LEAST;
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s);
