@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -490,6 +491,15 @@ _ROPE = {"plain": ROPE_PLAIN, "linear": ROPE_LINEAR, "bands": ROPE_BANDS, "yarn"
 _I32 = torch.int32
 
 
+def _int32(x) -> int:
+    """x for an int32 argument: ctypes would cut 2^32 + 3 down to 3, so what is beyond the type
+    becomes its end, which a length or a window means anyway or the call refuses."""
+    if type(x) is int and -1 <= x <= 0x7fffffff:
+        return x
+    x = operator.index(x)
+    return max(-1, min(x, 0x7fffffff))
+
+
 def _refuse(t, name: str, dtype, shape, dev: int):
     """Raises what is wrong with the tensor, if anything is."""
     if not isinstance(t, torch.Tensor):
@@ -676,7 +686,7 @@ def fadkv_pages_advance(pt: PageTable, new_lens: torch.Tensor, max_tokens: Optio
     if out.lens.shape[0] != R or out.lens.get_device() != dev:
         raise ValueError(f"out must be for {R} rows on cuda:{dev}")
     st = lib().fadkv_pages_advance(
-        pt.ring.shape[0], pt.page_size, R, max_pages, new, pt.lens.data_ptr(),
+        pt.ring.shape[0], _int32(pt.page_size), R, max_pages, new, pt.lens.data_ptr(),
         pt.table.data_ptr(), pt.ring.data_ptr(), pt.ring_state.data_ptr(), tokens,
         out.lens.data_ptr(), out.ring_state.data_ptr(), out.cu.data_ptr(), out.status.data_ptr(),
         out.slots.data_ptr(), out.positions.data_ptr(), out.workspace.data_ptr(),
@@ -695,10 +705,11 @@ def fadkv_rope_freqs(rot_dim: int, base: float, kind: str = "plain", factor: flo
         high = 32.0 if kind == "yarn" else 4.0
     if kind not in _ROPE:
         raise ValueError(f"kind must be one of {', '.join(_ROPE)}, got {kind!r}")
-    host = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.float64)
+    rot_dim = _int32(int(rot_dim))
+    host = torch.empty(max(0, min(rot_dim, 65536)) // 2, dtype=torch.float64)
     buf = (ctypes.c_double * max(1, host.numel()))()
     mscale = ctypes.c_double(1.0)
-    st = lib().fadkv_rope_freqs(int(rot_dim), float(base), _ROPE[kind], float(factor), float(low),
+    st = lib().fadkv_rope_freqs(rot_dim, float(base), _ROPE[kind], float(factor), float(low),
                                 float(high), float(original_len), buf, ctypes.byref(mscale))
     if st != FADKV_OK:
         raise FadkvError("fadkv_rope_freqs", st)
@@ -772,8 +783,8 @@ def fadkv_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions
 
 def fadkv_attend_paged_workspace_bytes(pages: Pages, R: int, heads: int, max_len: int) -> int:
     out = ctypes.c_size_t(0)
-    st = lib().fadkv_attend_paged_workspace_bytes(ctypes.byref(pages.c()), int(R), int(heads),
-                                                  int(max_len), ctypes.byref(out))
+    st = lib().fadkv_attend_paged_workspace_bytes(ctypes.byref(pages.c()), int(R), _int32(heads),
+                                                  _int32(max_len), ctypes.byref(out))
     if st != FADKV_OK:
         raise FadkvError("fadkv_attend_paged_workspace_bytes", st)
     return int(out.value)
@@ -820,8 +831,8 @@ def fadkv_attend_paged(pages: Pages, table: torch.Tensor, lens: torch.Tensor, q:
         need = fadkv_attend_paged_workspace_bytes(pages, R, heads, max_len)
         workspace = torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
     ws = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    st = lib().fadkv_attend_paged(ctypes.byref(p), tp, max_pages, lp, R, qp, heads, scale, window,
-                                  sinks, max_len, op, ws, workspace.numel(), _raw_stream(dev))
+    st = lib().fadkv_attend_paged(ctypes.byref(p), tp, max_pages, lp, R, qp, heads, scale,
+                                  _int32(window), _int32(sinks), _int32(max_len), op, ws, workspace.numel(), _raw_stream(dev))
     if st != FADKV_OK:
         raise FadkvError("fadkv_attend_paged", st)
     return out
@@ -831,7 +842,8 @@ def fadkv_attend_prompt_workspace_bytes(pages: Pages, R: int, n: int, heads: int
                                         max_len: int) -> int:
     out = ctypes.c_size_t(0)
     st = lib().fadkv_attend_prompt_workspace_bytes(ctypes.byref(pages.c()), int(R), int(n),
-                                                   int(heads), int(max_len), ctypes.byref(out))
+                                                   _int32(heads), _int32(max_len),
+                                                   ctypes.byref(out))
     if st != FADKV_OK:
         raise FadkvError("fadkv_attend_prompt_workspace_bytes", st)
     return int(out.value)
@@ -855,12 +867,15 @@ def fadkv_attend_prompt(pages: Pages, table: torch.Tensor, lens: torch.Tensor, c
         max_len = max_pages * p.page_size
     if workspace is None:
         need = fadkv_attend_prompt_workspace_bytes(pages, R, n, heads, max_len)
-        ws, need = (torch.empty(need, dtype=torch.uint8, device=q.device).data_ptr(), need) \
-            if need else (None, 0)
+        ws = None
+        if need:   # held until the call has launched: another thread could be given it
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
     else:
         ws, need = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
     st = lib().fadkv_attend_prompt(ctypes.byref(p), tp, max_pages, lp, cp, R, qp, n, heads, scale,
-                                   window, sinks, max_len, op, ws, need, _raw_stream(dev))
+                                   _int32(window), _int32(sinks), _int32(max_len), op, ws, need,
+                                   _raw_stream(dev))
     if st != FADKV_OK:
         raise FadkvError("fadkv_attend_prompt", st)
     return out

@@ -280,3 +280,8 @@ def test_prompt_kernels_use_m0_for_their_copies_alone(tmp_path):
             assert lines[i + 2].startswith("global_load_lds_dwordx4 "), lines[i + 2]
             copies += 1
         assert copies > 0
+
+
+def test_rope_freqs_number_past_32_bits_is_refused():
+    with pytest.raises(fadkv.FadkvError):
+        fadkv.fadkv_rope_freqs(2 ** 32 + 64, 10000.0, device="cpu")

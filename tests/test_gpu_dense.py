@@ -711,6 +711,53 @@ def test_attend_prompt_full_of_nan_ends():
     assert fadkv.fadkv_attend_prompt(pages, table, _i32([1500]), _i32([0, 1500]), q, 0.1).isnan().all()
 
 
+def test_numbers_past_32_bits_are_not_cut():
+    pages = fadkv.Pages.empty(4, 2, 16, 64, torch.float16, DEV)
+    pages.k.normal_()
+    pages.v.normal_()
+    table, lens, cu = _i32([[3, 1], [0, 2]]), _i32([20, 32]), _i32([0, 1, 2])
+    q = torch.randn(2, 4, 64, device=DEV, dtype=torch.float16)
+    for call in (lambda **kw: fadkv.fadkv_attend_paged(pages, table, lens, q, 0.125, **kw),
+                 lambda **kw: fadkv.fadkv_attend_prompt(pages, table, lens, cu, q, 0.125, **kw)):
+        whole = call()
+        assert torch.equal(call(window=2 ** 32 + 3), whole)
+        assert torch.equal(call(window=5, sinks=2 ** 32 + 1), whole)
+        for kw in ({"max_len": 2 ** 32 + 32}, {"window": -2 ** 32}, {"window": 3, "sinks": -2 ** 32}):
+            with pytest.raises(fadkv.FadkvError):
+                call(**kw)
+        with pytest.raises(TypeError):
+            call(window=1.5)
+
+
+def test_own_workspaces_are_held_while_a_call_launches(monkeypatch):
+    """Another thread's call may allocate between a call's allocation and its launch."""
+    pages = fadkv.Pages.empty(64, 2, 16, 64, torch.float16, DEV)
+    pages.k.normal_()
+    pages.v.normal_()
+    table, lens, cu = _i32(np.arange(64)[None]), _i32([1024]), _i32([0, 1])
+    q = torch.randn(1, 4, 64, device=DEV, dtype=torch.float16)
+    out = torch.empty_like(q)
+    real, held = fadkv.lib(), {}
+
+    class Watched:
+        def __getattr__(self, name):
+            f = getattr(real, name)
+
+            def call(*args):
+                held[name] = torch.cuda.memory_allocated()
+                return f(*args)
+            return call
+
+    monkeypatch.setattr(fadkv, "lib", Watched)
+    before = torch.cuda.memory_allocated()
+    fadkv.fadkv_attend_paged(pages, table, lens, q, 0.125, out=out)
+    fadkv.fadkv_attend_prompt(pages, table, lens, cu, q, 0.125, out=out)
+    assert fadkv.fadkv_attend_paged_workspace_bytes(pages, 1, 4, 1024) > 0
+    assert fadkv.fadkv_attend_prompt_workspace_bytes(pages, 1, 1, 4, 1024) > 0
+    assert held["fadkv_attend_paged"] > before
+    assert held["fadkv_attend_prompt"] > before
+
+
 def test_binding_refusals():
     _banner("binding refusals")
     pages, table = _cache("f16", 1, 64, 16, [20])
