@@ -3,7 +3,7 @@
 // A row's (token, query head of the group) pairs, token by token, are the columns: the `group` query
 // heads of a kv head share every key and value read.
 //
-// 16-bit types (attend_prompt_mfma_kernel): bound by the matrix cores and the vector unit, 4 d flops
+// attend_prompt_mfma_kernel, 16-bit types: bound by the matrix cores and the vector unit, 4 d flops
 // and one exponential per column and visible token.  A wave holds 32 columns, and the workgroup's
 // four waves share tiles of 64 tokens that come into LDS by direct copies.  As in attend_tile.h the
 // scores are computed transposed (S^T = K Q^T, v_mfma_f32_32x32x16), so that a lane's p are its
@@ -15,8 +15,12 @@
 // 8192 tokens, 32 query and 8 kv heads of 128 in bf16: 540 to 575 us, 0.96 to 1.02 PFLOP/s, where the
 // library's 8192^3 product reaches 1.2; two waves a SIMD overlap their matrix and vector instructions
 // in part, and the clock falls to 2.0 GHz.
-// fp32 (attend_prompt_kernel): a wave holds 16 columns and walks tiles of 32 tokens in registers; 81
-// TFLOP/s at the same shape, the library's product 154.
+// fp32: the same with tiles of 32 tokens and v_mfma_f32_32x32x2, bound by the matrix cores: a product
+// takes two keys, 4 apart as the scores lie, and a lane reads neighbouring elements of a key's value, one
+// for each block of d.  4120 us, 133 TFLOP/s at the same shape (the library's product 154), where 16
+// columns a wave with tiles in registers, each wave reading keys and values for itself, take 6800.
+// Rows of few columns in fp32 (attend_prompt_few_kernel) do take those 16 columns a wave: half a block of
+// 32 would be idle, and no tile waits for a barrier.
 #include "attend_tile.h"
 #include "tiles.h"
 
@@ -24,13 +28,16 @@ namespace fadkv {
 
 namespace {
 
-constexpr int PR_WAVES = 4;     // fp32: 16 columns a wave
-constexpr int PM_WAVES = 4;     // 16 bits: 32 columns a wave
+constexpr int PM_WAVES = 4;     // 32 columns a wave
+constexpr int PR_WAVES = 4;     // fp32, few columns: 16 columns a wave
+// Columns of a row, on average, up to which they are few (16 and 32 columns a wave: 64 rows of 4 columns
+// 73 and 156 us, 5 of 148 35 and 41, 8 of 512 44 and 43 at d = 128, 2 of 500 45 and 55, 3 of 1000 248
+// and 188, 3 of 2967 370 and 211).
+constexpr int PR_FEW = 512;
 // Few columns do not fill the chip: their tokens are then split over workgroups and joined, until
-// the two workgroups a CU holds are all there or a share falls to PR_LEAST (PM_LEAST) tokens.
+// the two workgroups a CU holds are all there or a share falls to this many tokens.
 constexpr int PM_FILL = 512;
-constexpr int PR_LEAST = 64;
-constexpr int PM_LEAST = 256;
+constexpr int least_share(int dtype) { return dtype == DT_F32 ? 64 : 256; }
 
 // Workgroup -> (row, block of `per` columns).  Row r's blocks are numbered from
 // floor(cu[r] * group / per) + r, which leaves room for all of them (ceil(x) <= floor(b) - floor(a) + 1
@@ -102,7 +109,7 @@ __device__ __forceinline__ void split_tiles(int count, int splits, int split, in
 
 // `blk` is kv head, then split, then block of columns, the first fastest
 template <int DT, int D, bool SPLIT>
-__global__ __launch_bounds__(64 * PR_WAVES) void attend_prompt_kernel(AttendArgs a) {
+__global__ __launch_bounds__(64 * PR_WAVES) void attend_prompt_few_kernel(AttendArgs a) {
   using T = AttTile<DT, D>;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -142,7 +149,7 @@ __global__ __launch_bounds__(64 * PR_WAVES) void attend_prompt_kernel(AttendArgs
   const Tiles tl = tiles_between(any, a.sinks, 32);
   const auto start_of = [&](int i) { return (i < tl.first ? i : tl.from + i - tl.first) * 32; };
   int i0 = 0, i1 = tl.count;
-  if constexpr (SPLIT) split_tiles(tl.count, a.splits, split, PR_LEAST / 32, i0, i1);
+  if constexpr (SPLIT) split_tiles(tl.count, a.splits, split, least_share(DT) / 32, i0, i1);
 
   AttState<DT, D> st;
   st.clear();
@@ -186,18 +193,19 @@ __global__ __launch_bounds__(64 * PR_WAVES) void attend_prompt_kernel(AttendArgs
   }
 }
 
-// ---- 16-bit types: LDS tiles of 64 tokens, v_mfma_f32_32x32x16 --------------------------------
-
 namespace {
-
-constexpr int PT = 64;   // tokens per tile
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
 template <int DT>
 __device__ __forceinline__ void mfma32(const uint4 &a, const uint4 &b, float16_t &c) {
-  if constexpr (DT == DT_F16)
+  if constexpr (DT == DT_F32) {
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+  } else if constexpr (DT == DT_F16)
     c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a),
                                                __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
   else
@@ -206,11 +214,13 @@ __device__ __forceinline__ void mfma32(const uint4 &a, const uint4 &b, float16_t
 }
 
 // Where the 16-byte chunk c of row r of a tile lies in its row.  Keys: a fragment read takes one
-// chunk of 16 rows, values: two 32-byte pieces of 4 rows; both then hit distinct banks.
-template <int D> __device__ __forceinline__ int key_swz(int r) {
-  return D == 128 ? (r & 15) : ((r >> 1) & 7);
+// chunk of 16 rows, values in 16 bits: two 32-byte pieces of 4 rows; both then hit distinct banks.
+// Values in fp32 are read in whole rows.
+template <int ROWB> __device__ __forceinline__ int key_swz(int r) {
+  return ROWB >= 256 ? (r & 15) : ((r >> 1) & 7);
 }
-template <int D> __device__ __forceinline__ int value_swz(int r) {
+template <int DT, int D> __device__ __forceinline__ int value_swz(int r) {
+  if (DT == DT_F32) return 0;
   return D == 128 ? ((r & 3) << 1) : (((r >> 1) & 1) << 1);
 }
 
@@ -227,16 +237,19 @@ __device__ __forceinline__ void lds_barrier() {
 
 template <int DT, int D, int WAVES, bool SPLIT>
 __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(AttendArgs a) {
-  constexpr int ROWB = 2 * D;
+  constexpr bool F32 = DT == DT_F32;
+  constexpr int PT = F32 ? 32 : 64;      // tokens per tile
+  constexpr int SB = PT / 32;            // 32-token score blocks
+  constexpr int ROWB = D * Elem<DT>::bytes;
   constexpr int CPR = ROWB / 16;         // chunks per row
   constexpr int NB = D / 32;             // 32-element blocks of d
-  constexpr int KC = D / 16;             // products per 32-token score block
+  constexpr int KC = ROWB / 32;          // 16-byte chunks of a row per lane
   constexpr int TILE = PT * ROWB;        // bytes of a K or V tile
   constexpr int ROWS_W = PT / WAVES;     // rows of a tile that a wave copies
   constexpr int LOADS = ROWS_W * ROWB / 1024;
   static_assert(ROWS_W <= 16 && LOADS >= 1, "a wave copies rows of one 16-token group");
   __shared__ __attribute__((aligned(256))) uint8_t s_kv[2][2][TILE];   // [stage][K, V]
-  // [stage][16-token group]: 1, no valid page; 2, an infinity or NaN that only some columns see
+  // [stage][wave's rows]: 1, no valid page; 2, an infinity or NaN that only some columns see
   __shared__ __attribute__((aligned(16))) int s_miss[2][4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -277,13 +290,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   const Visible all = {lo_of(w1), w0 + 1};                      // every column of the wave sees
   const size_t qi = (size_t)(rb.begin + tok) * heads + (size_t)head * a.group + gq;
 
-  // queries: entry 8 h + j of product i is element 16 i + 8 h + j.  The score's sign goes into q, so
+  // queries: entry 8 h + j of product i is element 16 i + 8 h + j (fp32: entry h of four products of
+  // two, 4 j + i, is element 8 j + 4 h + i).  The score's sign goes into q, so
   // that a column's largest score is its largest product.
   const bool flat = __builtin_fabsf(a.scale) < 1e-37f;   // all scores 0
   uint4 q[KC];
   {
     const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) + qi * ROWB);
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+    const uint32_t flip = a.scale < 0.f ? (F32 ? 0x80000000u : 0x80008000u) : 0u;
     const bool zero = !there || flat;
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
@@ -300,7 +314,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   const Tiles tl = tiles_between(any, a.sinks, PT);
   const auto start_of = [&](int i) { return (i < tl.first ? i : tl.from + i - tl.first) * PT; };
   int i0 = 0, count = tl.count;   // tiles [i0, count)
-  if constexpr (SPLIT) split_tiles(tl.count, a.splits, split, PM_LEAST / PT, i0, count);
+  if constexpr (SPLIT) split_tiles(tl.count, a.splits, split, least_share(DT) / PT, i0, count);
 
   // this wave's rows of a tile: ROWS_W of the 16-token group grp
   const int grp = wave * ROWS_W / 16;
@@ -311,8 +325,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   for (int j = 0; j < LOADS; ++j) {
     const int at = 64 * j + lane;
     const int r = row0 + at / CPR, c = at % CPR;
-    koff[j] = (uint32_t)((r - grp * 16) * ROWB + (c ^ key_swz<D>(r)) * 16);
-    voff[j] = (uint32_t)((r - grp * 16) * ROWB + (c ^ value_swz<D>(r)) * 16);
+    koff[j] = (uint32_t)((r - grp * 16) * ROWB + (c ^ key_swz<ROWB>(r)) * 16);
+    voff[j] = (uint32_t)((r - grp * 16) * ROWB + (c ^ value_swz<DT, D>(r)) * 16);
   }
   // Byte offset of the wave's group of tile i, or -1; asked for tile after tile.  A lane holds the
   // page of one of the next 64 tiles, so that no tile waits for its table entry.
@@ -329,7 +343,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
     for (int j = 0; j < LOADS; ++j) tile::copy16_to_lds(src, koff[j], dst + 1024u * j);
   };
   const auto copy_values = [&](int stage, int64_t at) {
-    if (lane == 0) s_miss[stage][grp] = at < 0;
+    if (lane == 0) s_miss[stage][wave] = at < 0;
     if (at < 0) return;
     const uint8_t *src = tile::uniform_ptr(pv.v + at);
     const uint32_t dst = lds0 + (uint32_t)stage * 2 * TILE + TILE + (uint32_t)row0 * ROWB;
@@ -359,7 +373,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
           *at16 = make_uint4(0, 0, 0, 0);
         }
       }
-      if (__any(bad != 0) && lane == 0) s_miss[stage][grp] = 2;
+      if (__any(bad != 0) && lane == 0) s_miss[stage][wave] = 2;
     }
     tile::wait_lds();
   };
@@ -372,10 +386,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   float m = -__builtin_inff(), base = 0.f, l = 0.f;   // m in units of 1 / scale2
 
   // the lane's byte offsets within a tile
-  int kaddr[2];
+  int kaddr[SB];
 #pragma unroll
-  for (int kb = 0; kb < 2; ++kb) kaddr[kb] = (32 * kb + col) * ROWB;
-  const int kswz = key_swz<D>(col);   // the same for col + 32
+  for (int kb = 0; kb < SB; ++kb) kaddr[kb] = (32 * kb + col) * ROWB;
+  const int kswz = key_swz<ROWB>(col);   // the same for col + 32
   // transposing read: lane 4 j + c of a 16-lane group gives key j's piece c, and gets element lane of
   // the four keys.  Row r of block b of V^T is element D/2 ((r >> 2) & 1) + 16 b + 4 (r >> 3) +
   // (r & 3), which leaves a lane with D/2 neighbouring elements of the output.
@@ -384,10 +398,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   const int vel = (D / 2) * ((vr >> 2) & 1) + 4 * (vr >> 3);     // element of block 0
 
   // the scores of the tile whose keys lie in `stage`
-  const auto scores = [&](int stage, float16_t (&s)[2]) {
+  const auto scores = [&](int stage, float16_t (&s)[SB]) {
     const uint8_t *kt = s_kv[stage][0];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < SB; ++kb) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[kb][e] = 0.f;
 #pragma unroll
@@ -402,7 +416,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   // copied two tiles ahead, values one.
   const int64_t at_v = group_offset(i0);
   int64_t at_k = group_offset(i0 + 1);
-  float16_t s[2];
+  float16_t s[SB];
   bool fine = true;
   if (i0 < count) {
     copy_keys(0, at_v);
@@ -432,17 +446,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
       const int at = t0 + 4 * h;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
+        constexpr int EG = 4 * SB;   // entries of a wave's rows
         const Visible c = {see.lo - at, gone[g] ? -1 : see.hi - at};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool seen = sees(c, a.sinks - at, 16 * g + 8 * (e >> 2) + (e & 3));
-          s[g >> 1][8 * (g & 1) + e] = seen ? s[g >> 1][8 * (g & 1) + e] : -__builtin_inff();
+        for (int e = EG * g; e < EG * g + EG; ++e) {
+          const bool seen = sees(c, a.sinks - at, 8 * (e >> 2) + (e & 3));
+          s[e >> 4][e & 15] = seen ? s[e >> 4][e & 15] : -__builtin_inff();
         }
       }
     }
     float top = s[0][0];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < SB; ++kb)
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kb][e]);
     if (__any(top * scale2 > m + 8.f)) {
@@ -460,42 +475,69 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
     }
     if (i + 1 < count) copy_values(stage ^ 1, at_now);
     __builtin_amdgcn_iglp_opt(0);   // LDS reads and products in turn: 551 -> 543 us at 8192 tokens
-    float16_t next[2];
+    float16_t next[SB];
     scores(stage ^ 1, next);   // behind the last tile: of old keys, not used
     const uint8_t *vt = s_kv[stage][1];
-    uint4 p[4];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float x[16];
+    if constexpr (F32) {
+      // product e takes the two halves' keys 8 (e >> 2) + 4 h + (e & 3), which is where p lies; a lane
+      // reads NB neighbouring elements of its key, one for each block of d
+      float sum = 0.f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        x[e] = __builtin_amdgcn_exp2f(fmaf(s[kb][e], scale2, -base));
-        l += x[e];
+        s[0][e] = __builtin_amdgcn_exp2f(fmaf(s[0][e], scale2, -base));
+        sum += s[0][e];
+      }
+      l += sum;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint8_t *src = vt + (8 * (e >> 2) + 4 * h + (e & 3)) * ROWB + 4 * NB * col;
+        float w[NB];
+        if constexpr (NB == 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(src);
+          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2 *>(src);
+          w[0] = x.x; w[1] = x.y;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          o[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(w[b], s[0][e], o[b], 0, 0, 0);
+      }
+    } else {
+      uint4 p[4];
+#pragma unroll
+      for (int kb = 0; kb < SB; ++kb) {
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[e] = __builtin_amdgcn_exp2f(fmaf(s[kb][e], scale2, -base));
+          l += x[e];
+        }
+#pragma unroll
+        for (int g2 = 0; g2 < 2; ++g2)
+          p[2 * kb + g2] = make_uint4(round2<DT>(x[8 * g2], x[8 * g2 + 1]), round2<DT>(x[8 * g2 + 2], x[8 * g2 + 3]),
+                                      round2<DT>(x[8 * g2 + 4], x[8 * g2 + 5]), round2<DT>(x[8 * g2 + 6], x[8 * g2 + 7]));
       }
 #pragma unroll
-      for (int g2 = 0; g2 < 2; ++g2)
-        p[2 * kb + g2] = make_uint4(round2<DT>(x[8 * g2], x[8 * g2 + 1]), round2<DT>(x[8 * g2 + 2], x[8 * g2 + 3]),
-                                    round2<DT>(x[8 * g2 + 4], x[8 * g2 + 5]), round2<DT>(x[8 * g2 + 6], x[8 * g2 + 7]));
-    }
+      for (int g2 = 0; g2 < 4; ++g2) {
 #pragma unroll
-    for (int g2 = 0; g2 < 4; ++g2) {
+        for (int b = 0; b < NB; ++b) {
+          uint2 w[2];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint2 w[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int r = 16 * g2 + 8 * u + vkey;
-          const int el = vel + 16 * b;
-          const uint8_t *src = vt + r * ROWB + (((el >> 3) ^ value_swz<D>(vkey)) << 4) + ((el & 7) << 1);
-          w[u] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)src));
+          for (int u = 0; u < 2; ++u) {
+            const int r = 16 * g2 + 8 * u + vkey;
+            const int el = vel + 16 * b;
+            const uint8_t *src = vt + r * ROWB + (((el >> 3) ^ value_swz<DT, D>(vkey)) << 4) + ((el & 7) << 1);
+            w[u] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)src));
+          }
+          mfma32<DT>(make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), p[g2], o[b]);
         }
-        mfma32<DT>(make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), p[g2], o[b]);
       }
     }
     if (i + 1 < count) settle(i + 1, stage ^ 1, at_now);
     lds_barrier();
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) s[kb] = next[kb];
+    for (int kb = 0; kb < SB; ++kb) s[kb] = next[kb];
   }
   if (!fine) {
     for (int c = 0; c < 32 && c0 + c < cols; ++c) {
@@ -510,61 +552,82 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_prompt_mfma_kernel(Atten
   }
   if (!there) return;
   l += other_half(l);
-  if constexpr (SPLIT) {
-    const size_t at = qi * a.splits + split;
+  const float inv = SPLIT ? 1.f : (l == 0.f ? 0.f : 1.f / l);   // no visible token: 0
+  const size_t at = SPLIT ? qi * a.splits + split : qi;
+  if (SPLIT && h == 0) a.part_ml[at] = make_float2(m, l);
+  if constexpr (F32) {   // entry e of block b is element NB (8 (e >> 2) + 4 h + (e & 3)) + b
+    float *dst = (SPLIT ? a.part_o : static_cast<float *>(a.out)) + at * D + 4 * NB * h;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float *to = dst + NB * (8 * (e >> 2) + (e & 3));
+      if constexpr (NB == 4)
+        *reinterpret_cast<float4 *>(to) = make_float4(o[0][e] * inv, o[1][e] * inv, o[2][e] * inv, o[3][e] * inv);
+      else
+        *reinterpret_cast<float2 *>(to) = make_float2(o[0][e] * inv, o[1][e] * inv);
+    }
+  } else if constexpr (SPLIT) {
     float4 *dst = reinterpret_cast<float4 *>(a.part_o + at * D + h * (D / 2));
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         dst[4 * b + u] = make_float4(o[b][4 * u], o[b][4 * u + 1], o[b][4 * u + 2], o[b][4 * u + 3]);
-    if (h == 0) a.part_ml[at] = make_float2(m, l);
-    return;
+  } else {
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at * ROWB + h * D);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = o[b][8 * u + e] * inv;
+        dst[2 * b + u] = make_uint4(round2<DT>(x[0], x[1]), round2<DT>(x[2], x[3]),
+                                    round2<DT>(x[4], x[5]), round2<DT>(x[6], x[7]));
+      }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;   // no visible token: 0
-  uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + qi * ROWB + h * D);
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = o[b][8 * u + e] * inv;
-      dst[2 * b + u] = make_uint4(round2<DT>(x[0], x[1]), round2<DT>(x[2], x[3]),
-                                  round2<DT>(x[4], x[5]), round2<DT>(x[6], x[7]));
-    }
+}
+
+static bool few_columns(int dtype, int64_t R, int64_t n, int32_t group) {
+  return dtype == DT_F32 && n * group <= PR_FEW * (R < n ? R : n);
 }
 
 // columns per workgroup
-static int prompt_columns(int dtype) { return dtype == DT_F32 ? 16 * PR_WAVES : 32 * PM_WAVES; }
+static int prompt_columns(int dtype, int64_t R, int64_t n, int32_t group) {
+  return few_columns(dtype, R, n, group) ? 16 * PR_WAVES : 32 * PM_WAVES;
+}
 
 int attend_prompt_splits(int dtype, int64_t R, int64_t n, int32_t kv_heads, int32_t group,
                          int64_t visible) {
-  const int64_t wgs = (n * group / prompt_columns(dtype) + (R < n ? R : n)) * kv_heads;
+  const int64_t wgs =
+      (n * group / prompt_columns(dtype, R, n, group) + (R < n ? R : n)) * kv_heads;
   int64_t s = wgs > 0 ? PM_FILL / wgs : 1;
-  const int64_t least = dtype == DT_F32 ? PR_LEAST : PM_LEAST;
+  const int64_t least = least_share(dtype);
   const int64_t most = (visible + least - 1) / least;
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s);
 }
 
+template <int DT, int D, bool SPLIT>
+static void attend_prompt_run(const AttendArgs &a, hipStream_t stream) {
+  // the blocks' numbers end below floor(n * group / columns) + R (find_row)
+  const int64_t wgs = (a.n * a.group / prompt_columns(DT, a.R, a.n, a.group) + a.R) * a.kv_heads;
+  const dim3 grid((unsigned)(wgs * a.splits));
+  if constexpr (DT == DT_F32)
+    if (few_columns(DT, a.R, a.n, a.group)) {
+      hipLaunchKernelGGL((attend_prompt_few_kernel<DT, D, SPLIT>), grid, dim3(64 * PR_WAVES), 0, stream, a);
+      return;
+    }
+  hipLaunchKernelGGL((attend_prompt_mfma_kernel<DT, D, PM_WAVES, SPLIT>), grid, dim3(64 * PM_WAVES), 0,
+                     stream, a);
+}
+
 template <int DT, int D>
 static hipError_t attend_prompt_run(const AttendArgs &a, hipStream_t stream) {
-  // the blocks' numbers end below floor(n * group / columns) + R (find_row)
-  const int64_t wgs = (a.n * a.group / prompt_columns(DT) + a.R) * a.kv_heads;
-  const dim3 grid((unsigned)(wgs * a.splits));
-  if constexpr (DT == DT_F32) {
-    const dim3 block(64 * PR_WAVES);
-    if (a.splits > 1) hipLaunchKernelGGL((attend_prompt_kernel<DT, D, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((attend_prompt_kernel<DT, D, false>), grid, block, 0, stream, a);
-  } else {
-    const dim3 block(64 * PM_WAVES);
-    if (a.splits > 1)
-      hipLaunchKernelGGL((attend_prompt_mfma_kernel<DT, D, PM_WAVES, true>), grid, block, 0, stream, a);
-    else
-      hipLaunchKernelGGL((attend_prompt_mfma_kernel<DT, D, PM_WAVES, false>), grid, block, 0, stream, a);
+  if (a.splits > 1) {
+    attend_prompt_run<DT, D, true>(a, stream);
+    return launch_attend_join(DT, D, a, a.n * a.kv_heads * a.group, stream);
   }
-  if (a.splits > 1) return launch_attend_join(DT, D, a, a.n * a.kv_heads * a.group, stream);
+  attend_prompt_run<DT, D, false>(a, stream);
   return hipGetLastError();
 }
 

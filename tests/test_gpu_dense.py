@@ -6,7 +6,8 @@ the output type (eps / 2) once at the end:
   reciprocal, two factors, cosine (its argument is rounded, pi u, and 2 u of its own), mscale, a
   product and a sum: 20 u of |a| + |b|;
 * attention: a score is off by (d + 4) u sum|q k| scale and two more u of itself, p and the sum
-  each by that and 4 u, the running sums by (tokens / 32 + 64) u at most; p is rounded once more
+  each by that and 4 u, the running sums by (tokens / 32 + 64) u at most (tokens / 2 in the fp32 form
+  of many columns, whose matrix instruction adds two tokens a step); p is rounded once more
   to 16-bit types, in fp16 by 2^-25 of the largest p at least (its smallest numbers).
 """
 import numpy as np
@@ -289,10 +290,10 @@ def _gathered(pages, table, r, tokens):
     return K, V, there
 
 
-def _check_query(got, q, pos, K, V, there, scale, window, sinks, dt, what):
+def _check_query(got, q, pos, K, V, there, scale, window, sinks, dt, what, step=32):
     ref, size, top, raw = dense_oracle.attend_query(q, pos, K, V, there, scale, window, sinks)
     d = q.shape[0]
-    e = 2 * ((d + 4) * raw + 4 * top + 4) * U + (K.shape[0] / 32 + 64) * U
+    e = 2 * ((d + 4) * raw + 4 * top + 4) * U + (K.shape[0] / step + 64) * U
     u = _half_step(dt)
     tol = u * np.abs(ref) * 1.01 + e * size
     if dt != torch.float32:
@@ -414,7 +415,7 @@ def test_attend_paged_beyond_32_bits():
     assert torch.equal(pages.k[16999, :, 255], kvs[0]) and torch.equal(pages.v[16999, :, 255], kvs[0])
 
 
-def _check_prompt(dt, kv, group, d, page, cached, fresh, window=0, sinks=0, seed=0, pad=0):
+def _check_prompt(dt, kv, group, d, page, cached, fresh, window=0, sinks=0, seed=0, pad=0, step=32):
     lens = np.asarray(cached) + np.asarray(fresh)
     pages, table = _cache(dt, kv, d, page, lens, seed=seed)
     cu = np.concatenate([[0], np.cumsum(fresh)])
@@ -437,7 +438,7 @@ def _check_prompt(dt, kv, group, d, page, cached, fresh, window=0, sinks=0, seed
         for i in at:
             for h in range(kv * group):
                 _check_query(got[cu[r] + i, h], _f64(q[cu[r] + i, h]), cached[r] + i, K[:, h // group],
-                             V[:, h // group], there, scale, window, sinks, TORCH[dt], (r, i, h))
+                             V[:, h // group], there, scale, window, sinks, TORCH[dt], (r, i, h), step)
 
 
 PROMPT = [
@@ -477,6 +478,30 @@ LONG = [
 def test_attend_prompt_split(dt, kv, group, d, page, cached, fresh, window, sinks, pad):
     _banner(f"prompt split {dt} kv={kv}x{group} d={d} {cached}+{fresh} window={window}/{sinks}")
     _check_prompt(dt, kv, group, d, page, cached, fresh, window, sinks, seed=d + page, pad=pad)
+
+
+MANY = [
+    # fp32, rows of more than 512 columns on average: 32 columns a wave
+    (2, 4, 128, 16, [0], [257], 0, 0, 3),
+    (1, 3, 64, 32, [0, 700, 31], [400, 190, 1], 0, 0, 0),
+    (1, 8, 128, 64, [65, 0], [130, 33], 40, 5, 2),
+    (1, 2, 64, 16, [1100], [300], 500, 70, 0),
+    (3, 5, 64, 256, [255, 1], [258, 257], 1, 0, 0),
+    (8, 4, 64, 16, [0], [700], 0, 0, 0),       # no split
+    (1, 1, 128, 16, [5, 0, 900], [1000, 0, 600], 0, 0, 1),
+]
+
+
+@pytest.mark.parametrize("kv,group,d,page,cached,fresh,window,sinks,pad", MANY)
+def test_attend_prompt_many_columns_in_fp32(kv, group, d, page, cached, fresh, window, sinks, pad):
+    _banner(f"prompt f32 kv={kv}x{group} d={d} page={page} {cached}+{fresh} window={window}/{sinks}")
+    _check_prompt("f32", kv, group, d, page, cached, fresh, window, sinks, seed=d + page, pad=pad, step=2)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("cached,fresh,window,sinks", [(100, 400, 60, 7), (0, 400, 0, 0)])
+def test_attend_prompt_of_many_columns_keeps_what_is_not_seen_away(dt, cached, fresh, window, sinks):
+    test_attend_prompt_keeps_what_is_not_seen_away(dt, cached, fresh, window, sinks)
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
